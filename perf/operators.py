@@ -82,7 +82,7 @@ def draw(rng):
                     slots=B + rng.randint(0, 40), gate=rng.random() < 0.7)
     D = 8 * _between(rng, 8, 1024)
     post, pre = rng.choice(((True, True), (True, True), (True, False), (False, True)))
-    return dict(op=op, dtype=dtype, res=rng.choice(("bf16", "f32")), M=_between(rng, 1, (16384 * 2048) // D), D=D,
+    return dict(op=op, dtype=dtype, res=rng.choice(("bf16", "f32")), M=_between(rng, 1, (16384 * 2048) // (D * WIDTH[dtype] // 2)), D=D,
                 gate=rng.choice(("none", "silu", "sigmoid", "linear")), first=rng.random() < 0.4, post=post, pre=pre)
 
 
