@@ -289,7 +289,7 @@ def _own_run(s):
     op = s["op"]
     if op == "norm":
         c = s["case"]
-        act = {"none": A.GATE_SILU, "silu": A.GATE_SILU, "sigmoid": A.GATE_SIGMOID, "linear": A.GATE_LINEAR}[c["gate"]]
+        act = {"none": A.ACT_SILU, "silu": A.ACT_SILU, "sigmoid": A.ACT_SIGMOID, "linear": A.ACT_LINEAR}[c["gate"]]
         A.block_norm(s["y"], s["res"], s["res_out"], s["h"], w_post=s["w_post"], w_pre=s["w_pre"], gate=s["gate"],
                      gate_act=act, gate_first=c["first"], alpha=s["alpha"], eps=s["eps"])
         return [s["res_out"], s["h"]] if c["pre"] else [s["res_out"]]
