@@ -18,9 +18,15 @@
  *   [pith, params]   pith.science review, "Assumptions & free parameters"
  *                    (Mamba selective SSM, Section 3.2 Eq. 3; P, L, offset = layer index)
  *
+ * Beside them stand the operators of a Mamba block in its uncompressed form (the
+ * same selective SSM, [pith, params]): the short causal convolution ahead of the
+ * SSM, the selective scan over whole sequences with skip, gate and carried state,
+ * their single-token steps, and the norms around a block.
+ *
  * Conventions for every call
- *   - Every tensor pointer is caller-owned DEVICE memory, row-major, contiguous,
- *     16-byte aligned.  The library allocates nothing and keeps no state
+ *   - Every tensor pointer is caller-owned DEVICE memory, row-major, contiguous
+ *     (rows may be further apart where the call takes a row stride `ld...`, in
+ *     elements), 16-byte aligned.  The library allocates nothing and keeps no state
  *     between calls; it is thread-safe.
  *   - Every call is asynchronous on the given stream (a cudaStream_t; NULL is
  *     the legacy default stream) and never synchronizes.  The scans and the
@@ -72,6 +78,9 @@ typedef enum { ATTAMBA_MASK_TRAIN = 0, ATTAMBA_MASK_TEST = 1 } attamba_mask_t;
                                       ATTAMBA_CHECKED): an index fell outside the array it addresses;
                                       the access was skipped (a TMA load, which reads the fill value
                                       out of range, is reported and still made) */
+
+#define ATTAMBA_DEV_BAD_SEQS 0x10  /* a sequence table's cu is not 0 = cu[0] <= ... <= cu[S] <= T, a slot lies
+                                      outside [-1, n_slots), or a call names one slot twice */
 
 /* Compact per-query key index built by attamba_chunk_index [pith, carries]:
  * query i (sequence-relative position) of sequence b reads
@@ -294,6 +303,95 @@ attamba_status_t attamba_decode_step_noalloc(attamba_dtype_t dtype, const attamb
                                              const void* C_k, const void* B_v, const void* C_v,
                                              float scale, void* o_t, int32_t* d_status,
                                              attamba_stream_t stream);
+
+/* Sequences of a packed batch of prompts and where their carried states live.
+ * Sequence s owns tokens [cu[s], cu[s+1]); empty ones are allowed.  Rows of the
+ * token arrays from cu[S] on belong to none: their outputs are left as they are.
+ * A malformed cu raises ATTAMBA_DEV_BAD_SEQS and leaves the outputs undefined (every
+ * access stays inside the arrays).  A sequence whose slot is out of range, or was
+ * named by an earlier sequence, raises it too and runs as if its slot were -1. */
+typedef struct {
+  const int32_t* cu;    /* [S + 1] first token of each sequence, cu[0] = 0, cu[S] <= T */
+  const int32_t* slots; /* nullable [S] state row of each sequence, -1: none (it starts from zero and keeps
+                           nothing); NULL: sequence s has row s */
+  const int32_t* cont;  /* nullable [S] nonzero: the sequence continues from its state row; NULL: none does */
+  int64_t T;            /* rows of the token arrays, 1 <= T < 2^31 - 65536 */
+  int32_t S;            /* sequences, 1 <= S <= 2^24 */
+} attamba_seqs_t;
+
+/* Activation of a convolution or a gate. */
+typedef enum { ATTAMBA_ACT_LINEAR = 0, ATTAMBA_ACT_SILU = 1, ATTAMBA_ACT_SIGMOID = 2 } attamba_act_t;
+
+/* attamba_causal_conv -- short causal depthwise convolution over packed prompts.
+ * [pith, params] (Mamba's block: the SSM input passes a short convolution first):
+ *     y[t,d] = act(bias[d] + sum_{k < K} w[d,k] x[t-(K-1)+k, d])
+ * where positions ahead of a sequence's first token come from its state row if it
+ * continues and are 0 otherwise.  Afterwards its state row holds its last K-1 inputs.
+ *   x, y     [T, D], row strides ldx, ldy;  w [D, K] f32, K = 2, 3 or 4;  bias nullable [D] f32.
+ *   act      ATTAMBA_ACT_LINEAR or ATTAMBA_ACT_SILU.
+ *   state    nullable [n_slots, K-1, D] of dtype, oldest input first, updated in place.
+ * D a multiple of 8, row strides of a multiple of 16 bytes.  y overlaps no input. */
+attamba_status_t attamba_causal_conv(attamba_dtype_t dtype, const void* x, int64_t ldx, const float* w,
+                                     const float* bias, int32_t D, int32_t K, attamba_act_t act,
+                                     const attamba_seqs_t* seqs, void* state, int32_t n_slots, void* y,
+                                     int64_t ldy, int32_t* d_status, attamba_stream_t stream);
+
+/* attamba_conv_step -- attamba_causal_conv for one new token of each of B sequences that continue.
+ *   x, y   [B, D], row strides ldx, ldy;  slots nullable [B]: -1 marks a row that only fills the
+ *          batch up (its y is left as it is); NULL: row b has state row b.
+ * A slot out of range or named by an earlier row raises ATTAMBA_DEV_BAD_SEQS; that row is skipped. */
+attamba_status_t attamba_conv_step(attamba_dtype_t dtype, const void* x, int64_t ldx, const float* w,
+                                   const float* bias, int32_t D, int32_t K, attamba_act_t act, int32_t B,
+                                   const int32_t* slots, void* state, int32_t n_slots, void* y, int64_t ldy,
+                                   int32_t* d_status, attamba_stream_t stream);
+
+/* Bytes of device workspace attamba_selective_scan needs for T token rows (0 for sizes out of range). */
+size_t attamba_selective_scan_workspace_size(int64_t T, int32_t D, int32_t N);
+
+/* attamba_selective_scan -- the selective SSM over packed prompts, state carried over whole sequences.
+ * [pith, params] Mamba selective SSM (Section 3.2, Eq. 3) with its skip and gate.  Per token t, channel d:
+ *     delta = softplus(dt[t,d] + bias[d])
+ *     h[:,d] = exp(delta A[d,:]) h[:,d] + delta x[t,d] B[t,:]
+ *     y[t,d] = (sum_n C[t,n] h[n,d] + skip[d] x[t,d]) silu(z[t,d])
+ * h starts from the sequence's state row if it continues and from 0 otherwise; afterwards the row holds h.
+ *   x, dt, z, y [T, D] (z nullable: no gate);  B, C [T, N];  each with a row stride.
+ *   bias, skip  nullable [D] f32;  A [D, N] f32 (negative);  N 16 or 32;  D a multiple of 8.
+ *   state       nullable [n_slots, N, D] f32, updated in place.
+ *   workspace   device scratch of at least attamba_selective_scan_workspace_size(T, D, N) bytes;
+ *               calls that can overlap on the GPU need one each.
+ * Row strides of a multiple of 16 bytes.  y overlaps no input. */
+attamba_status_t attamba_selective_scan(attamba_dtype_t dtype, const void* x, int64_t ldx, const void* dt,
+                                        int64_t lddt, const float* bias, const float* A, const void* B,
+                                        int64_t ldb, const void* C, int64_t ldc, const float* skip, const void* z,
+                                        int64_t ldz, int32_t D, int32_t N, const attamba_seqs_t* seqs, float* state,
+                                        int32_t n_slots, void* y, int64_t ldy, void* workspace,
+                                        size_t workspace_bytes, int32_t* d_status, attamba_stream_t stream);
+
+/* attamba_scan_step -- attamba_selective_scan for one new token of each of `rows` sequences that continue.
+ *   x, dt, z, y [rows, D];  B, C [rows, N];  slots as in attamba_conv_step. */
+attamba_status_t attamba_scan_step(attamba_dtype_t dtype, const void* x, int64_t ldx, const void* dt, int64_t lddt,
+                                   const float* bias, const float* A, const void* B, int64_t ldb, const void* C,
+                                   int64_t ldc, const float* skip, const void* z, int64_t ldz, int32_t D, int32_t N,
+                                   int32_t rows, const int32_t* slots, float* state, int32_t n_slots, void* y,
+                                   int64_t ldy, int32_t* d_status, attamba_stream_t stream);
+
+/* attamba_block_norm -- the norms after a block and before the next, with gate, residual scale and sum.
+ * Per row, with norm(v, w) = v rsqrt(mean(v^2) + eps) w:
+ *     v = y;  gate_first: v = v act(gate);  w_post: v = norm(v, w_post);  not gate_first: v = v act(gate)
+ *     r = res + alpha scale v          -> res_out
+ *     h = norm(r, w_pre)               -> h
+ * Every part but one output may be left out (NULL): no y (r = res: a norm before the first block), no gate,
+ * no w_post, no res (r = alpha scale v), no scale; h and w_pre go together.  The norm before the next block
+ * reads r before its rounding to res_dtype.
+ *   dtype      type of y, gate and h;  res_dtype  type of res and res_out (F32 or BF16 each).
+ *   y, gate, res, res_out, h  [M, D], each with a row stride;  w_post, scale, w_pre [D] f32;  eps >= 0.
+ * D a multiple of 8, at most 32768; row strides of a multiple of 16 bytes.  res_out may be res and h may be
+ * y (same address, stride and type); nothing else may overlap an output. */
+attamba_status_t attamba_block_norm(attamba_dtype_t dtype, attamba_dtype_t res_dtype, const void* y, int64_t ldy,
+                                    const void* gate, int64_t ldg, attamba_act_t act, int32_t gate_first,
+                                    const float* w_post, const void* res, int64_t ldr, const float* scale,
+                                    float alpha, const float* w_pre, float eps, int64_t M, int32_t D, void* res_out,
+                                    int64_t ldro, void* h, int64_t ldh, attamba_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -22,14 +22,17 @@ LIB_PATH = os.path.join(_HERE, "libattamba_checked.so" if os.environ.get("ATTAMB
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA = 0, 1, 2, 3
 F32, BF16 = 0, 1
 MASK_TRAIN, MASK_TEST = 0, 1
-DEV_BAD_CHUNKS, DEV_CACHE_FULL, DEV_TIMEOUT, DEV_BOUNDS = 0x1, 0x2, 0x4, 0x8
+ACT_LINEAR, ACT_SILU, ACT_SIGMOID = 0, 1, 2
+DEV_BAD_CHUNKS, DEV_CACHE_FULL, DEV_TIMEOUT, DEV_BOUNDS, DEV_BAD_SEQS = 0x1, 0x2, 0x4, 0x8, 0x10
 
 # every symbol include/attamba.h declares
 EXPORTS = ("attamba_version", "attamba_status_string", "attamba_last_error",
            "attamba_uniform_chunk_count", "attamba_chunk_index", "attamba_kv_ssm_scan",
            "attamba_chunk_attn_fwd", "attamba_cache_bytes", "attamba_selftest_wait_timeout", "attamba_decode_workspace_size", "attamba_decode_step",
            "attamba_decode_step_noalloc", "attamba_cache_from_prefill",
-           "attamba_kv_ssm_scan_u", "attamba_proj_gemm")
+           "attamba_kv_ssm_scan_u", "attamba_proj_gemm", "attamba_causal_conv", "attamba_conv_step",
+           "attamba_selective_scan_workspace_size", "attamba_selective_scan", "attamba_scan_step",
+           "attamba_block_norm")
 
 
 class AttambaError(RuntimeError):
@@ -51,6 +54,11 @@ class CacheT(ctypes.Structure):
                 ("bpos", ctypes.c_void_p), ("Kr", ctypes.c_void_p), ("Vr", ctypes.c_void_p),
                 ("nb", ctypes.c_void_p), ("pos", ctypes.c_void_p)] + \
                [(k, ctypes.c_int32) for k in ("B", "H", "dh", "N", "P", "offset", "L", "cap")]
+
+
+class SeqsT(ctypes.Structure):
+    _fields_ = [("cu", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("cont", ctypes.c_void_p),
+                ("T", ctypes.c_int64), ("S", ctypes.c_int32)]
 
 
 _lib = None
@@ -96,6 +104,22 @@ def load():
     L.attamba_decode_step_noalloc.argtypes = [ctypes.c_int, ctypes.POINTER(CacheT)] + [vp] * 12 + [f32, vp, vp, vp]
     L.attamba_cache_from_prefill.restype = ctypes.c_int
     L.attamba_cache_from_prefill.argtypes = [ctypes.c_int, ctypes.POINTER(CacheT)] + [vp] * 13 + [i32, vp, vp]
+    L.attamba_causal_conv.restype = ctypes.c_int
+    L.attamba_causal_conv.argtypes = [ctypes.c_int, vp, i64, vp, vp, i32, i32, ctypes.c_int, ctypes.POINTER(SeqsT),
+                                      vp, i32, vp, i64, vp, vp]
+    L.attamba_conv_step.restype = ctypes.c_int
+    L.attamba_conv_step.argtypes = [ctypes.c_int, vp, i64, vp, vp, i32, i32, ctypes.c_int, i32, vp, vp, i32, vp, i64,
+                                    vp, vp]
+    L.attamba_selective_scan_workspace_size.restype = sz
+    L.attamba_selective_scan_workspace_size.argtypes = [i64, i32, i32]
+    scan_args = [ctypes.c_int, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp, i64, i32, i32]
+    L.attamba_selective_scan.restype = ctypes.c_int
+    L.attamba_selective_scan.argtypes = scan_args + [ctypes.POINTER(SeqsT), vp, i32, vp, i64, vp, sz, vp, vp]
+    L.attamba_scan_step.restype = ctypes.c_int
+    L.attamba_scan_step.argtypes = scan_args + [i32, vp, vp, i32, vp, i64, vp, vp]
+    L.attamba_block_norm.restype = ctypes.c_int
+    L.attamba_block_norm.argtypes = [ctypes.c_int, ctypes.c_int, vp, i64, vp, i64, ctypes.c_int, i32, vp, vp, i64, vp,
+                                     f32, vp, f32, i64, i32, vp, i64, vp, i64, vp]
     _lib = L
     return L
 
@@ -316,3 +340,181 @@ def proj_gemm(X, W, outs, status=None, stream=None):
     st = load().attamba_proj_gemm(BF16, _ptr(X, bf, "X"), _ptr(W, bf, "W"), M, Nout, K, segs, len(outs),
                                   _ptr(status, torch.int32, "status", allow_none=True), _stream(stream))
     _check(st, "attamba_proj_gemm")
+
+
+# ---------------------------------------------------------------- the SSM block's operators
+# These take token rows [rows, cols] whose rows may be further apart than cols (column slices of a wide
+# projection), and run on the device of their tensors whichever device is current.
+
+def _rows(t, like, rows, cols, name, dtype=None):
+    """(device pointer, row stride) of a [rows, cols] tensor on ``like``'s device; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype != (like.dtype if dtype is None else dtype):
+        raise AttambaError(f"{name} must be {like.dtype if dtype is None else dtype}, got {t.dtype}")
+    if t.device != like.device:
+        raise AttambaError(f"{name} must be on {like.device}, got {t.device}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise AttambaError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    if t.stride(1) != 1 and cols > 1:
+        raise AttambaError(f"{name} must have its columns next to each other")
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+
+def _dense(t, like, shape, dtype, name):
+    """Device pointer of a contiguous tensor of this shape on ``like``'s device; None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_contiguous():
+        raise AttambaError(f"{name} must be a contiguous {dtype} {list(shape)} on {like.device}, got "
+                           f"{t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _on_cuda(t, name):
+    if not t.is_cuda:
+        raise AttambaError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.dim() != 2 or t.shape[0] < 1:
+        raise AttambaError(f"{name} must be [rows >= 1, cols], got {list(t.shape)}")
+
+
+def _call(fn, what, like, status, stream, *args, with_status=True):
+    """fn(*args, [status,] stream) with ``like``'s device current."""
+    dev = like.device
+    if with_status:
+        args += (_dense(status, like, (1,), torch.int32, "status"),)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise AttambaError(f"{what}: the stream is on {stream.device}, the tensors on {dev}")
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    if st != OK:
+        _check(st, what)
+
+
+class Seqs:
+    """The sequences of a packed batch of prompts (see attamba_seqs_t): ``cu`` [S + 1] int32 offsets into the
+    T token rows, ``slots`` [S] the state row of each sequence (-1: none; None: row s for sequence s), ``cont``
+    [S] non-zero where the sequence continues from its state row (None: none does)."""
+
+    def __init__(self, cu, T, slots=None, cont=None):
+        i32 = torch.int32
+        if cu.dim() != 1 or cu.numel() < 2 or cu.dtype != i32 or not cu.is_cuda or not cu.is_contiguous():
+            raise AttambaError("cu must be a contiguous CUDA int32 [S + 1]")
+        self.S, self.T = cu.numel() - 1, int(T)
+        self.cu, self.slots, self.cont = cu, slots, cont
+        self._c = SeqsT(cu.data_ptr(), _dense(slots, cu, (self.S,), i32, "slots"),
+                        _dense(cont, cu, (self.S,), i32, "cont"), self.T, self.S)
+        self._ref = ctypes.byref(self._c)
+
+    def c_ref(self, like):
+        if self.cu.device != like.device:
+            raise AttambaError(f"the sequence table must be on {like.device}, got {self.cu.device}")
+        if self.T != like.shape[0]:
+            raise AttambaError(f"the sequence table is for {self.T} token rows, got {like.shape[0]}")
+        return self._ref
+
+
+def _state(state, like, rows, dtype, name="state"):
+    """(device pointer, slots) of a contiguous [slots, rows, D] state; (None, 0) for None."""
+    if state is None:
+        return None, 0
+    n = state.shape[0] if state.dim() else 0
+    return _dense(state, like, (n, rows, like.shape[1]), dtype, name), n
+
+
+def _conv_args(x, w, bias, state, y):
+    _on_cuda(x, "x")
+    T, D = x.shape
+    if w.dim() != 2:
+        raise AttambaError("w must be [D, K]")
+    K = w.shape[1]
+    f32 = torch.float32
+    px, ldx = _rows(x, x, T, D, "x")
+    py, ldy = _rows(y, x, T, D, "y")
+    pst, n = _state(state, x, K - 1, x.dtype)
+    return (_dtype_code(x), px, ldx, _dense(w, x, (D, K), f32, "w"), _dense(bias, x, (D,), f32, "bias"), D, K,
+            pst, n, py, ldy)
+
+
+def causal_conv(x, w, bias, seqs, y, state=None, act=ACT_SILU, status=None, stream=None):
+    """attamba_causal_conv: y [T, D] = act(bias + short causal depthwise convolution of x [T, D]) over the
+    sequences of ``seqs``.  w [D, K] f32 (K 2 to 4), bias [D] f32 or None, state [slots, K - 1, D] or None."""
+    code, px, ldx, pw, pb, D, K, pst, n, py, ldy = _conv_args(x, w, bias, state, y)
+    _call(load().attamba_causal_conv, "attamba_causal_conv", x, status, stream, code, px, ldx, pw, pb, D, K, act,
+          seqs.c_ref(x), pst, n, py, ldy)
+
+
+def conv_step(x, w, bias, state, y, slots=None, act=ACT_SILU, status=None, stream=None):
+    """attamba_conv_step: causal_conv for one new token of each row of x [B, D]; ``slots`` [B] int32 names the
+    rows' state rows (-1: a row that only fills the batch up; None: row b for row b)."""
+    code, px, ldx, pw, pb, D, K, pst, n, py, ldy = _conv_args(x, w, bias, state, y)
+    _call(load().attamba_conv_step, "attamba_conv_step", x, status, stream, code, px, ldx, pw, pb, D, K, act,
+          x.shape[0], _dense(slots, x, (x.shape[0],), torch.int32, "slots"), pst, n, py, ldy)
+
+
+def _scan_args(x, dt, bias, A, B, C, skip, z):
+    _on_cuda(x, "x")
+    T, D = x.shape
+    if A.dim() != 2:
+        raise AttambaError("A must be [D, N]")
+    N = A.shape[1]
+    f32 = torch.float32
+    return (_dtype_code(x), *_rows(x, x, T, D, "x"), *_rows(dt, x, T, D, "dt"), _dense(bias, x, (D,), f32, "bias"),
+            _dense(A, x, (D, N), f32, "A"), *_rows(B, x, T, N, "B"), *_rows(C, x, T, N, "C"),
+            _dense(skip, x, (D,), f32, "skip"), *_rows(z, x, T, D, "z"), D, N)
+
+
+def selective_scan_workspace_size(T, D, N):
+    return int(load().attamba_selective_scan_workspace_size(T, D, N))
+
+
+def selective_scan(x, dt, bias, A, B, C, seqs, y, skip=None, z=None, state=None, workspace=None, status=None,
+                   stream=None):
+    """attamba_selective_scan: the selective SSM over the sequences of ``seqs``.  x, dt, z, y [T, D]; B, C [T, N];
+    A [D, N] f32; bias, skip [D] f32 or None; z None: no gate; state [slots, N, D] f32 or None; workspace:
+    selective_scan_workspace_size(T, D, N) bytes (None where that is 0)."""
+    args = _scan_args(x, dt, bias, A, B, C, skip, z)
+    py, ldy = _rows(y, x, x.shape[0], x.shape[1], "y")
+    pst, n = _state(state, x, A.shape[1], torch.float32)
+    pws, size = None, 0
+    if workspace is not None:
+        size = workspace.numel() * workspace.element_size()
+        pws = _dense(workspace, x, workspace.shape, workspace.dtype, "workspace")
+    _call(load().attamba_selective_scan, "attamba_selective_scan", x, status, stream, *args, seqs.c_ref(x), pst, n, py,
+          ldy, pws, size)
+
+
+def scan_step(x, dt, bias, A, B, C, state, y, skip=None, z=None, slots=None, status=None, stream=None):
+    """attamba_scan_step: selective_scan for one new token of each row of x [B, D]; ``slots`` as in conv_step."""
+    args = _scan_args(x, dt, bias, A, B, C, skip, z)
+    py, ldy = _rows(y, x, x.shape[0], x.shape[1], "y")
+    pst, n = _state(state, x, A.shape[1], torch.float32)
+    _call(load().attamba_scan_step, "attamba_scan_step", x, status, stream, *args, x.shape[0],
+          _dense(slots, x, (x.shape[0],), torch.int32, "slots"), pst, n, py, ldy)
+
+
+def block_norm(y, res, res_out=None, h=None, w_post=None, w_pre=None, gate=None, gate_act=ACT_SILU, gate_first=False,
+               scale=None, alpha=1.0, eps=1e-5, stream=None):
+    """attamba_block_norm: the norms after a block (w_post) and before the next (w_pre) with its gate, residual
+    scale and sum: res_out = res + alpha scale norm(y) act(gate), h = norm(res_out).  Row tensors [M, D]; y or res
+    may be None, and either output; the weights and scale are [D] f32."""
+    first = y if y is not None else res
+    if first is None:
+        raise AttambaError("block_norm needs y or res")
+    _on_cuda(first, "y" if y is not None else "res")
+    M, D = first.shape
+    f32 = torch.float32
+    typed = y if y is not None else h if h is not None else res         # the type of y, gate and h
+    rtyped = res if res is not None else res_out if res_out is not None else typed
+    args = (*_rows(y, first, M, D, "y"), *_rows(gate, first, M, D, "gate", typed.dtype), int(gate_act),
+            int(bool(gate_first)), _dense(w_post, first, (D,), f32, "w_post"),
+            *_rows(res, first, M, D, "res", rtyped.dtype), _dense(scale, first, (D,), f32, "scale"), float(alpha),
+            _dense(w_pre, first, (D,), f32, "w_pre"), float(eps), M, D,
+            *_rows(res_out, first, M, D, "res_out", rtyped.dtype), *_rows(h, first, M, D, "h", typed.dtype))
+    _call(load().attamba_block_norm, "attamba_block_norm", first, None, stream, _dtype_code(typed), _dtype_code(rtyped),
+          *args, with_status=False)

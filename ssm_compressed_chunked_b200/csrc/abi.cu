@@ -336,4 +336,195 @@ attamba_status_t attamba_decode_step_noalloc(attamba_dtype_t dtype, const attamb
   return e == cudaSuccess ? ATTAMBA_OK : cuda_fail(e, "attamba_decode_step_noalloc");
 }
 
+namespace {
+// Token rows an operator of the SSM block reads or writes: rows x cols elements of `es` bytes, `ld` apart.
+struct Rows {
+  const void* p;
+  int64_t rows, ld;
+  int32_t cols;
+  int es;
+  bool out;
+  const char* name;
+};
+bool ok_rows(const Rows& r) {
+  return aligned16(r.p) && r.ld >= r.cols && r.ld < ((int64_t)1 << 31) && (r.ld * r.es) % 16 == 0;
+}
+// whether two row sets share a byte: column windows of one wide array (same stride) do not
+bool overlap(const Rows& a, const Rows& b) {
+  const int64_t as = a.ld * a.es, bs = b.ld * b.es, ac = (int64_t)a.cols * a.es, bc = (int64_t)b.cols * b.es;
+  const intptr_t pa = reinterpret_cast<intptr_t>(a.p), pb = reinterpret_cast<intptr_t>(b.p);
+  const intptr_t ea = pa + (a.rows - 1) * as + ac, eb = pb + (b.rows - 1) * bs + bc;
+  if (ea <= pb || eb <= pa) return false;
+  if (as != bs) return true;
+  const int64_t off = (((pb - pa) % as) + as) % as;   // b's window starts `off` bytes into a's row
+  return off < ac || off + bc > as;
+}
+// every given row set is well formed and no output shares memory with another set
+attamba_status_t check_rows(const Rows* r, int n, const char* what) {
+  for (int i = 0; i < n; ++i) {
+    if (!r[i].p) continue;
+    if (!ok_rows(r[i])) {
+      snprintf(g_err, sizeof(g_err), "%s: %s must be 16-byte aligned with a row stride of a multiple of 16 bytes", what,
+               r[i].name);
+      return ATTAMBA_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < n; ++j)
+      if (j != i && r[i].out && r[j].p && overlap(r[i], r[j])) {
+        snprintf(g_err, sizeof(g_err), "%s: %s overlaps %s", what, r[i].name, r[j].name);
+        return ATTAMBA_ERR_INVALID_ARG;
+      }
+  }
+  return ATTAMBA_OK;
+}
+int elem_size(attamba_dtype_t d) { return d == ATTAMBA_BF16 ? 2 : 4; }
+constexpr int64_t kMaxSeqTokens = ((int64_t)1 << 31) - 65536;   // token positions plus a tile stay int32
+constexpr int32_t kMaxChannels = 1 << 20;
+constexpr int32_t kMaxRows = 1 << 24;                           // sequences or batch rows of one call
+bool ok_channels(int32_t D) { return D >= 8 && D % 8 == 0 && D <= kMaxChannels; }
+bool ok_seqs(const attamba_seqs_t* q) {
+  return q && q->cu && q->T >= 1 && q->T < kMaxSeqTokens && q->S >= 1 && q->S <= kMaxRows;
+}
+
+attamba_status_t conv_entry(attamba_dtype_t dtype, attamba::ConvArgs& a, int64_t ldx, int64_t ldy, int32_t K,
+                            attamba_act_t act, bool step, cudaStream_t s, const char* name) {
+  if (!ok_dtype(dtype) || K < 2 || K > 4) return ATTAMBA_ERR_UNSUPPORTED;
+  if (!a.x || !a.w || !a.y || !ok_channels(a.D) || (act != ATTAMBA_ACT_LINEAR && act != ATTAMBA_ACT_SILU))
+    return ATTAMBA_ERR_INVALID_ARG;
+  if ((a.state && a.n_slots < 1) || !aligned16(a.w) || !aligned16(a.bias) || !aligned16(a.state))
+    return ATTAMBA_ERR_INVALID_ARG;
+  const int es = elem_size(dtype);
+  const Rows rows[] = {{a.x, a.T, ldx, a.D, es, false, "x"},
+                       {a.y, a.T, ldy, a.D, es, true, "y"},
+                       {a.state, (int64_t)a.n_slots * (K - 1), a.D, a.D, es, true, "state"}};
+  const attamba_status_t st = check_rows(rows, 3, name);
+  if (st != ATTAMBA_OK) return st;
+  a.ldx = (int32_t)ldx;
+  a.ldy = (int32_t)ldy;
+  a.act = (int32_t)act;
+  const cudaError_t e = step ? attamba::launch_conv_step(dtype, K, a, s) : attamba::launch_causal_conv(dtype, K, a, s);
+  return e == cudaSuccess ? ATTAMBA_OK : cuda_fail(e, name);
+}
+
+attamba_status_t check_scan(attamba_dtype_t dtype, attamba::SelScanArgs& a, int64_t ldx, int64_t lddt, int64_t ldb,
+                            int64_t ldc, int64_t ldz, int64_t ldy, const char* name) {
+  if (!ok_dtype(dtype) || (a.N != 16 && a.N != 32)) return ATTAMBA_ERR_UNSUPPORTED;
+  if (!a.x || !a.dt || !a.A || !a.Bm || !a.Cm || !a.y || !ok_channels(a.D)) return ATTAMBA_ERR_INVALID_ARG;
+  if (!aligned16(a.A) || !aligned16(a.bias) || !aligned16(a.skip) || (a.state && a.n_slots < 1))
+    return ATTAMBA_ERR_INVALID_ARG;
+  const int es = elem_size(dtype);
+  const Rows rows[] = {{a.x, a.T, ldx, a.D, es, false, "x"},   {a.dt, a.T, lddt, a.D, es, false, "dt"},
+                       {a.Bm, a.T, ldb, a.N, es, false, "B"},  {a.Cm, a.T, ldc, a.N, es, false, "C"},
+                       {a.z, a.T, ldz, a.D, es, false, "z"},   {a.y, a.T, ldy, a.D, es, true, "y"},
+                       {a.state, (int64_t)a.n_slots * a.N, a.D, a.D, 4, true, "state"}};
+  const attamba_status_t st = check_rows(rows, 7, name);
+  if (st != ATTAMBA_OK) return st;
+  a.ldx = (int32_t)ldx;
+  a.lddt = (int32_t)lddt;
+  a.ldb = (int32_t)ldb;
+  a.ldc = (int32_t)ldc;
+  a.ldz = (int32_t)ldz;
+  a.ldy = (int32_t)ldy;
+  return ATTAMBA_OK;
+}
+}  // namespace
+
+attamba_status_t attamba_causal_conv(attamba_dtype_t dtype, const void* x, int64_t ldx, const float* w,
+                                     const float* bias, int32_t D, int32_t K, attamba_act_t act,
+                                     const attamba_seqs_t* seqs, void* state, int32_t n_slots, void* y,
+                                     int64_t ldy, int32_t* d_status, attamba_stream_t stream) {
+  if (!ok_seqs(seqs)) return ATTAMBA_ERR_INVALID_ARG;
+  attamba::ConvArgs a{};
+  a.x = x; a.w = w; a.bias = bias; a.state = state; a.y = y;
+  a.cu = seqs->cu; a.slots = seqs->slots; a.cont = seqs->cont;
+  a.T = seqs->T; a.S = seqs->S; a.D = D; a.n_slots = n_slots; a.status = d_status;
+  return conv_entry(dtype, a, ldx, ldy, K, act, false, reinterpret_cast<cudaStream_t>(stream), "attamba_causal_conv");
+}
+
+attamba_status_t attamba_conv_step(attamba_dtype_t dtype, const void* x, int64_t ldx, const float* w,
+                                   const float* bias, int32_t D, int32_t K, attamba_act_t act, int32_t B,
+                                   const int32_t* slots, void* state, int32_t n_slots, void* y, int64_t ldy,
+                                   int32_t* d_status, attamba_stream_t stream) {
+  if (B < 1 || B > kMaxRows || !state) return ATTAMBA_ERR_INVALID_ARG;
+  attamba::ConvArgs a{};
+  a.x = x; a.w = w; a.bias = bias; a.state = state; a.y = y; a.slots = slots;
+  a.T = B; a.D = D; a.n_slots = n_slots; a.status = d_status;
+  return conv_entry(dtype, a, ldx, ldy, K, act, true, reinterpret_cast<cudaStream_t>(stream), "attamba_conv_step");
+}
+
+size_t attamba_selective_scan_workspace_size(int64_t T, int32_t D, int32_t N) {
+  if (T < 1 || T >= kMaxSeqTokens || !ok_channels(D) || (N != 16 && N != 32)) return 0;
+  return attamba::selective_scan_workspace_bytes(T, D, N);
+}
+
+attamba_status_t attamba_selective_scan(attamba_dtype_t dtype, const void* x, int64_t ldx, const void* dt,
+                                        int64_t lddt, const float* bias, const float* A, const void* B,
+                                        int64_t ldb, const void* C, int64_t ldc, const float* skip, const void* z,
+                                        int64_t ldz, int32_t D, int32_t N, const attamba_seqs_t* seqs, float* state,
+                                        int32_t n_slots, void* y, int64_t ldy, void* workspace,
+                                        size_t workspace_bytes, int32_t* d_status, attamba_stream_t stream) {
+  if (!ok_seqs(seqs)) return ATTAMBA_ERR_INVALID_ARG;
+  attamba::SelScanArgs a{};
+  a.x = x; a.dt = dt; a.Bm = B; a.Cm = C; a.z = z; a.bias = bias; a.A = A; a.skip = skip; a.state = state; a.y = y;
+  a.cu = seqs->cu; a.slots = seqs->slots; a.cont = seqs->cont;
+  a.T = seqs->T; a.S = seqs->S; a.D = D; a.N = N; a.n_slots = n_slots;
+  a.work = static_cast<float*>(workspace);
+  a.status = d_status;
+  const attamba_status_t st = check_scan(dtype, a, ldx, lddt, ldb, ldc, ldz, ldy, "attamba_selective_scan");
+  if (st != ATTAMBA_OK) return st;
+  const size_t need = attamba::selective_scan_workspace_bytes(a.T, D, N);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) {
+    snprintf(g_err, sizeof(g_err), "attamba_selective_scan: needs %zu bytes of workspace, 16-byte aligned", need);
+    return ATTAMBA_ERR_INVALID_ARG;
+  }
+  const cudaError_t e = attamba::launch_selective_scan(dtype, a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTAMBA_OK : cuda_fail(e, "attamba_selective_scan");
+}
+
+attamba_status_t attamba_scan_step(attamba_dtype_t dtype, const void* x, int64_t ldx, const void* dt, int64_t lddt,
+                                   const float* bias, const float* A, const void* B, int64_t ldb, const void* C,
+                                   int64_t ldc, const float* skip, const void* z, int64_t ldz, int32_t D, int32_t N,
+                                   int32_t rows, const int32_t* slots, float* state, int32_t n_slots, void* y,
+                                   int64_t ldy, int32_t* d_status, attamba_stream_t stream) {
+  if (rows < 1 || rows > kMaxRows || !state) return ATTAMBA_ERR_INVALID_ARG;
+  attamba::SelScanArgs a{};
+  a.x = x; a.dt = dt; a.Bm = B; a.Cm = C; a.z = z; a.bias = bias; a.A = A; a.skip = skip; a.state = state; a.y = y;
+  a.slots = slots;
+  a.T = rows; a.D = D; a.N = N; a.n_slots = n_slots; a.status = d_status;
+  const attamba_status_t st = check_scan(dtype, a, ldx, lddt, ldb, ldc, ldz, ldy, "attamba_scan_step");
+  if (st != ATTAMBA_OK) return st;
+  const cudaError_t e = attamba::launch_scan_step(dtype, a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTAMBA_OK : cuda_fail(e, "attamba_scan_step");
+}
+
+attamba_status_t attamba_block_norm(attamba_dtype_t dtype, attamba_dtype_t res_dtype, const void* y, int64_t ldy,
+                                    const void* gate, int64_t ldg, attamba_act_t act, int32_t gate_first,
+                                    const float* w_post, const void* res, int64_t ldr, const float* scale,
+                                    float alpha, const float* w_pre, float eps, int64_t M, int32_t D, void* res_out,
+                                    int64_t ldro, void* h, int64_t ldh, attamba_stream_t stream) {
+  if (!ok_dtype(dtype) || !ok_dtype(res_dtype)) return ATTAMBA_ERR_UNSUPPORTED;
+  if (D < 8 || D % 8 != 0 || M < 1 || M > 0x7fffffff) return ATTAMBA_ERR_INVALID_ARG;
+  if (D > attamba::kMaxNormDim) return ATTAMBA_ERR_UNSUPPORTED;
+  if (!(eps >= 0.f) || (!y && !res) || (!res_out && !h) || (h == nullptr) != (w_pre == nullptr))
+    return ATTAMBA_ERR_INVALID_ARG;
+  if (!y && (gate || w_post || scale)) return ATTAMBA_ERR_INVALID_ARG;
+  if (act != ATTAMBA_ACT_LINEAR && act != ATTAMBA_ACT_SILU && act != ATTAMBA_ACT_SIGMOID) return ATTAMBA_ERR_INVALID_ARG;
+  if (!aligned16(w_post) || !aligned16(scale) || !aligned16(w_pre)) return ATTAMBA_ERR_INVALID_ARG;
+  const int es = elem_size(dtype), rs = elem_size(res_dtype);
+  // an output in place of its input is written by the thread that read it, after the row's last read
+  const bool in_place_r = res_out && res_out == res && ldro == ldr, in_place_h = h && h == y && ldh == ldy;
+  const Rows rows[] = {{in_place_h ? nullptr : y, M, ldy, D, es, false, "y"},
+                       {gate, M, ldg, D, es, false, "gate"},
+                       {in_place_r ? nullptr : res, M, ldr, D, rs, false, "res"},
+                       {res_out, M, ldro, D, rs, true, "res_out"},
+                       {h, M, ldh, D, es, true, "h"}};
+  const attamba_status_t st = check_rows(rows, 5, "attamba_block_norm");
+  if (st != ATTAMBA_OK) return st;
+  attamba::NormArgs a{};
+  a.y = y; a.gate = gate; a.res = res; a.w_post = w_post; a.scale = scale; a.w_pre = w_pre; a.res_out = res_out; a.h = h;
+  a.ldy = ldy; a.ldg = ldg; a.ldr = ldr; a.ldro = ldro; a.ldh = ldh;
+  a.M = M; a.D = D; a.act = (int32_t)act; a.gate_first = gate_first; a.alpha = alpha; a.eps = eps;
+  const cudaError_t e = attamba::launch_block_norm(dtype, res_dtype, a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTAMBA_OK : cuda_fail(e, "attamba_block_norm");
+}
+
 }  // extern "C"

@@ -1,0 +1,167 @@
+// The norms after a block and before the next one, with the block's gate, the
+// residual scale and the residual sum, in one pass.
+//
+// Per row, with norm(v, w) = v rsqrt(mean(v^2) + eps) w:
+//     v = y [act(gate)];  v = norm(v, w_post);  v = v [act(gate)];
+//     r = res + alpha scale v;  h = norm(r, w_pre).
+//
+// Mapping (B200).  Memory-bound: y, gate and res read once, r and h written once.
+// A row belongs to one block of 32 to 1024 threads (several rows a block while a warp
+// holds a row); every thread has VPT vectors of 8 channels in fp32 registers
+// from the first load to the last store, so the two means cost two reductions and
+// no second read.  Sums of squares are fp32: a thread's share first, then the warp's
+// tree, then the warps' partial sums.
+#include "common.cuh"
+#include "launch.h"
+
+namespace attamba {
+
+namespace {
+// 8 channels
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ float act_f(int act, float g) {
+  if (act == ATTAMBA_ACT_LINEAR) return g;
+  const float s = __fdividef(1.f, 1.f + ex2(-g * kLog2e));
+  return act == ATTAMBA_ACT_SILU ? g * s : s;
+}
+
+// Sum over the row's threads (32: the warp; more: the block, through `part`).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  if (TPR == 32) return v;
+  __syncthreads();   // the partial sums of the sum before have been read
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+#pragma unroll
+  for (int w = 0; w < TPR / 32; ++w) v += part[w];
+  return v;
+}
+
+constexpr int kWarpRows = 4;   // rows a block while a warp holds a row
+
+template <typename T, typename R, int TPR, int VPT>
+__global__ void __launch_bounds__(TPR == 32 ? 32 * kWarpRows : TPR) block_norm_kernel(NormArgs p) {
+  __shared__ float part[TPR / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t row = TPR == 32 ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  if (row >= p.M) return;   // whole warps only: a block of more threads has one row, below M
+  const int id = threadIdx.x % TPR;
+  const int D = p.D;
+  float v[VPT][8];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int c = (id + k * TPR) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
+    if (p.y && c < D) load8(static_cast<const T*>(p.y) + row * p.ldy + c, v[k]);
+  }
+  auto gate = [&]() {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (id + k * TPR) * 8;
+      if (c < D) {
+        float g[8];
+        load8(static_cast<const T*>(p.gate) + row * p.ldg + c, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] *= act_f(p.act, g[i]);
+      }
+    }
+  };
+  auto norm = [&](const float* w) {
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(v[k][i], v[k][i], ss);
+    const float rs = rsqrtf(row_sum<TPR>(ss, part) / (float)D + p.eps);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (id + k * TPR) * 8;
+      if (c < D) {
+        float f[8];
+        load8(w + c, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] *= rs * f[i];
+      }
+    }
+  };
+  if (p.gate && p.gate_first) gate();
+  if (p.w_post) norm(p.w_post);
+  if (p.gate && !p.gate_first) gate();
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int c = (id + k * TPR) * 8;
+    if (c >= D) continue;
+    if (p.scale) {
+      float f[8];
+      load8(p.scale + c, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[k][i] *= f[i];
+    }
+    float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (p.res) load8(static_cast<const R*>(p.res) + row * p.ldr + c, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[k][i] = p.y ? fmaf(p.alpha, v[k][i], r[i]) : r[i];
+    if (p.res_out) store8(static_cast<R*>(p.res_out) + row * p.ldro + c, v[k]);
+  }
+  if (p.h) {
+    norm(p.w_pre);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (id + k * TPR) * 8;
+      if (c < D) store8(static_cast<T*>(p.h) + row * p.ldh + c, v[k]);
+    }
+  }
+}
+
+template <typename T, typename R, int TPR, int VPT>
+cudaError_t launch(const NormArgs& a, cudaStream_t s) {
+  const int64_t blocks = TPR == 32 ? (a.M + kWarpRows - 1) / kWarpRows : a.M;
+  return launch_dependent(block_norm_kernel<T, R, TPR, VPT>, dim3((unsigned)blocks), TPR == 32 ? 32 * kWarpRows : TPR, s, a);
+}
+
+template <typename T, typename R>
+cudaError_t launch_for(const NormArgs& a, cudaStream_t s) {
+  const int vecs = a.D / 8;
+  if (vecs <= 32) return launch<T, R, 32, 1>(a, s);
+  if (vecs <= 64) return launch<T, R, 32, 2>(a, s);
+  if (vecs <= 128) return launch<T, R, 128, 1>(a, s);
+  if (vecs <= 256) return launch<T, R, 256, 1>(a, s);
+  if (vecs <= 512) return launch<T, R, 256, 2>(a, s);
+  if (vecs <= 1024) return launch<T, R, 512, 2>(a, s);
+  if (vecs <= 2048) return launch<T, R, 1024, 2>(a, s);
+  return launch<T, R, 1024, 4>(a, s);
+}
+}  // namespace
+
+cudaError_t launch_block_norm(attamba_dtype_t dtype, attamba_dtype_t res_dtype, const NormArgs& a, cudaStream_t s) {
+  if (dtype == ATTAMBA_BF16)
+    return res_dtype == ATTAMBA_BF16 ? launch_for<__nv_bfloat16, __nv_bfloat16>(a, s) : launch_for<__nv_bfloat16, float>(a, s);
+  return res_dtype == ATTAMBA_BF16 ? launch_for<float, __nv_bfloat16>(a, s) : launch_for<float, float>(a, s);
+}
+
+}  // namespace attamba

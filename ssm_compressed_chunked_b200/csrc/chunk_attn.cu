@@ -110,7 +110,6 @@ constexpr uint32_t kSCol = 0;                               // S, two buffers: c
 constexpr uint32_t kPCol = 2 * kBN;                         // P, two buffers: columns 128..159, 160..191 (bf16 pairs)
 constexpr uint32_t kOCol = 3 * kBN;                         // O: columns 192..255 (fp32)
 constexpr uint64_t kWaitNs = 4000000000ull;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 static_assert(kOCol + kDH <= kTmemCols, "TMEM columns");
 

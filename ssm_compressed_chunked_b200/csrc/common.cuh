@@ -56,6 +56,81 @@ __device__ __forceinline__ uint64_t global_ns() {
   return t;
 }
 
+// ---------------------------------------------------------------- SSM arithmetic, sequence tables
+constexpr float kLog2e = 1.4426950408889634f;
+
+// two-wide fp32 arithmetic
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+
+// softplus(z) = log(1 + e^z) with u = e^z:  log2(1 + u) on the multi-function unit
+// when u >= 1/16 (its absolute error, about 2^-22, is then below 3e-6 of the
+// result), the series u - u^2/2 + u^3/3 - u^4/4 + u^5/5 below (truncation under
+// u^5/6 relative), and z itself above 20.
+__device__ __forceinline__ float softplus_f(float z) {
+  const float u = ex2(z * kLog2e);
+  float lg;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(1.f + u));
+  const float ser = u * fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0.2f, -0.25f), 1.f / 3.f), -0.5f), 1.f);
+  const float v = u < 0.0625f ? ser : lg * 0.6931471805599453f;
+  return z > 20.f ? z : v;
+}
+
+// silu(z) = z / (1 + e^-z); e^-z overflows to infinity for z < -88.7, the quotient is then -0
+__device__ __forceinline__ float silu_f(float z) { return __fdividef(z, 1.f + ex2(-z * kLog2e)); }
+
+// Number of entries of the ascending row p[0, n) that are below v, by all 32 lanes:
+// each round probes 32 evenly spaced entries and keeps the gap where the answer lies.
+__device__ __forceinline__ int count_below_warp(const int32_t* p, int n, int v, int lane) {
+  int l = 0, h = n;   // the answer lies in [l, h]
+  while (l < h) {
+    const int step = (h - l + 31) >> 5;
+    const int idx = l + lane * step;
+    const bool below = idx < h && p[idx] < v;
+    const int c = __popc(__ballot_sync(0xffffffffu, below));
+    if (c == 0) break;                       // p[l] >= v: the answer is l
+    const int nl = l + (c - 1) * step + 1;   // p[l + (c - 1) step] < v
+    h = min(h, l + c * step);                // p[l + c step] >= v, or the end
+    l = nl;
+  }
+  return l;
+}
+
+// Whether sequence (or batch row) s may use its state row: the slot lies in [0, n_slots) and no earlier
+// one has it.  By all 32 lanes; a wrong slot raises ATTAMBA_DEV_BAD_SEQS.  Returns the slot, or -1.
+__device__ __forceinline__ int state_slot_warp(const int32_t* slots, int s, int n_slots, int lane, int32_t* st) {
+  const int slot = slots ? slots[s] : s;
+  if (slot == -1) return -1;
+  bool bad = slot < 0 || slot >= n_slots;
+  if (slots && !bad)
+    for (int i = lane; i < s; i += 32) bad |= slots[i] == slot;
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0) raise_status(st, ATTAMBA_DEV_BAD_SEQS);
+    return -1;
+  }
+  return slot;
+}
+
+// Whether cu[0, S] is 0 = cu[0] <= ... <= cu[S] <= T; by one warp.
+__device__ __forceinline__ void check_sequences_warp(const int32_t* cu, int S, int64_t T, int lane, int32_t* st) {
+  bool bad = cu[0] != 0 || cu[S] > T;
+  for (int i = lane; i < S; i += 32) bad |= cu[i] > cu[i + 1];
+  if (__any_sync(0xffffffffu, bad) && lane == 0) raise_status(st, ATTAMBA_DEV_BAD_SEQS);
+}
+
 // ---------------------------------------------------------------- shared memory / mbarrier
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -60,7 +60,6 @@ constexpr int kStageKeys = 16 * kUnroll;                  // 4 warps x 4 lane gr
 constexpr int kStages = ATTAMBA_DECODE_STAGES;
 constexpr uint32_t kRowBytes = kDH * 2;                   // one bf16 key or value row
 constexpr uint32_t kStageBytes = kStageKeys * kRowBytes;  // per tensor
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct DecodeBars {
@@ -78,23 +77,6 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
                    smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
-}
-
-// Number of entries of the ascending row p[0, n) that are below v, by all 32 lanes:
-// each round probes 32 evenly spaced entries and keeps the gap where the answer lies.
-__device__ __forceinline__ int count_below_warp(const int32_t* p, int n, int v, int lane) {
-  int l = 0, h = n;   // the answer lies in [l, h]
-  while (l < h) {
-    const int step = (h - l + 31) >> 5;
-    const int idx = l + lane * step;
-    const bool below = idx < h && p[idx] < v;
-    const int c = __popc(__ballot_sync(0xffffffffu, below));
-    if (c == 0) break;                       // p[l] >= v: the answer is l
-    const int nl = l + (c - 1) * step + 1;   // p[l + (c - 1) step] < v
-    h = min(h, l + c * step);                // p[l + c step] >= v, or the end
-    l = nl;
-  }
-  return l;
 }
 
 __device__ __forceinline__ bool chunk_starts_at(int t, int P, int o) {

@@ -20,7 +20,6 @@ namespace attamba {
 
 namespace {
 constexpr int kDH = 64;
-constexpr float kLog2e = 1.4426950408889634f;
 
 // one past the first chunk end of a uniform chunking: the offset mod P, or P when that is 0
 __host__ __device__ __forceinline__ int32_t first_boundary_end(int32_t P, int32_t offset) {

@@ -65,7 +65,6 @@ constexpr int kScanThreads = 128;
 #endif
 constexpr int kStageTokens = 64;       // B/C staging window (even, so token pairs never straddle one)
 constexpr int kMaxChunksPerBlock = 256;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPolyMinExp = -125.f;
 // 2^f on [-1/2, 1/2], minimax relative error (own Remez fit), f32 coefficients
 constexpr float kP0 = 0.9999280571937561f;
@@ -73,21 +72,6 @@ constexpr float kP1 = 0.6932609677314758f;
 constexpr float kP2 = 0.2426111251115799f;
 constexpr float kP3 = 0.0551716685295105f;
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
-        "l"(reinterpret_cast<const uint64_t&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-  return d;
-}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
   asm("add.rn.f32x2 %0, %1, %2;"
@@ -116,19 +100,6 @@ __device__ __forceinline__ float2 exp2_poly2(float2 x) {
   // the low mantissa bits of t hold j; shifted into the exponent field they scale p by 2^j
   return make_float2(__uint_as_float(__float_as_uint(t.x) * 8388608u + __float_as_uint(p.x)),
                      __uint_as_float(__float_as_uint(t.y) * 8388608u + __float_as_uint(p.y)));
-}
-
-// softplus(z) = log(1 + e^z) with u = e^z:  log2(1 + u) on the multi-function unit
-// when u >= 1/16 (its absolute error, about 2^-22, is then below 3e-6 of the
-// result), the series u - u^2/2 + u^3/3 - u^4/4 + u^5/5 below (truncation under
-// u^5/6 relative), and z itself above 20.
-__device__ __forceinline__ float softplus_f(float z) {
-  const float u = ex2(z * kLog2e);
-  float lg;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(1.f + u));
-  const float ser = u * fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0.2f, -0.25f), 1.f / 3.f), -0.5f), 1.f);
-  const float v = u < 0.0625f ? ser : lg * 0.6931471805599453f;
-  return z > 20.f ? z : v;
 }
 
 template <typename T, int CPT> struct Vec;
