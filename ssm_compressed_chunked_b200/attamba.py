@@ -344,56 +344,76 @@ def proj_gemm(X, W, outs, status=None, stream=None):
 
 # ---------------------------------------------------------------- the SSM block's operators
 # These take token rows [rows, cols] whose rows may be further apart than cols (column slices of a wide
-# projection), and run on the device of their tensors whichever device is current.
+# projection), and run on the device of their tensors whichever device is current.  A decode step makes
+# several of these calls per layer and waits for the host, so the checks are few and flat: one pass over a
+# tensor's type, device, shape and strides, with the message made only when something is wrong.
 
-def _rows(t, like, rows, cols, name, dtype=None):
-    """(device pointer, row stride) of a [rows, cols] tensor on ``like``'s device; (None, 0) for None."""
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+# the current stream's handle by device index; torch.cuda.current_stream builds a Stream object (2 us)
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _rows(t, dtype, dev, shape, name):
+    """(device pointer, row stride) of a [rows, cols] tensor; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dtype != (like.dtype if dtype is None else dtype):
-        raise AttambaError(f"{name} must be {like.dtype if dtype is None else dtype}, got {t.dtype}")
-    if t.device != like.device:
-        raise AttambaError(f"{name} must be on {like.device}, got {t.device}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise AttambaError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-    if t.stride(1) != 1 and cols > 1:
-        raise AttambaError(f"{name} must have its columns next to each other")
-    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+        ld, unit = t.stride()
+        if unit == 1 or shape[1] == 1:
+            return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+    raise AttambaError(f"{name} must be {dtype} {list(shape)} on cuda:{dev} with its columns next to each other, got "
+                       f"{t.dtype} {list(t.shape)} on {t.device}, strides {t.stride()}")
 
 
-def _dense(t, like, shape, dtype, name):
-    """Device pointer of a contiguous tensor of this shape on ``like``'s device; None for None."""
+def _dense(t, dtype, dev, shape, name):
+    """Device pointer of a contiguous tensor; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != like.device or not t.is_contiguous():
-        raise AttambaError(f"{name} must be a contiguous {dtype} {list(shape)} on {like.device}, got "
-                           f"{t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    raise AttambaError(f"{name} must be a contiguous {dtype} {list(shape)} on cuda:{dev}, got {t.dtype} {list(t.shape)} "
+                       f"on {t.device}")
 
 
-def _on_cuda(t, name):
-    if not t.is_cuda:
+def _lead(t, name):
+    """(dtype code, dtype, device index, shape) of the tensor the others are checked against."""
+    dev, dtype, shape = t.get_device(), t.dtype, t.shape
+    if dev < 0:
         raise AttambaError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.dim() != 2 or t.shape[0] < 1:
-        raise AttambaError(f"{name} must be [rows >= 1, cols], got {list(t.shape)}")
+    if len(shape) != 2 or shape[0] < 1:
+        raise AttambaError(f"{name} must be [rows >= 1, cols], got {list(shape)}")
+    return BF16 if dtype is _BF16 else _dtype_code(t), dtype, dev, shape
 
 
-def _call(fn, what, like, status, stream, *args, with_status=True):
-    """fn(*args, [status,] stream) with ``like``'s device current."""
-    dev = like.device
-    if with_status:
-        args += (_dense(status, like, (1,), torch.int32, "status"),)
+def _state(state, dtype, dev, rows, cols):
+    """(device pointer, slots) of a contiguous [slots, rows, cols] state; (None, 0) for None."""
+    if state is None:
+        return None, 0
+    shape = state.shape
+    if len(shape) == 3 and shape[1] == rows and shape[2] == cols:
+        return _dense(state, dtype, dev, shape, "state"), shape[0]
+    raise AttambaError(f"state must be [slots, {rows}, {cols}], got {list(shape)}")
+
+
+def _call(fn, what, dev, stream, args):
+    """fn(*args, stream) with device ``dev`` current."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise AttambaError(f"{what}: the stream is on {stream.device}, the tensors on {dev}")
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
+        handle = _current_stream(dev)
+    elif stream.device.index == dev:
+        handle = stream.cuda_stream
+    else:
+        raise AttambaError(f"{what}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+    if dev == torch.cuda.current_device():
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, handle)
     if st != OK:
         _check(st, what)
+
+
+def _status(status, dev):
+    return None if status is None else _dense(status, _I32, dev, (1,), "status")
 
 
 class Seqs:
@@ -402,71 +422,58 @@ class Seqs:
     [S] non-zero where the sequence continues from its state row (None: none does)."""
 
     def __init__(self, cu, T, slots=None, cont=None):
-        i32 = torch.int32
-        if cu.dim() != 1 or cu.numel() < 2 or cu.dtype != i32 or not cu.is_cuda or not cu.is_contiguous():
+        if cu.dim() != 1 or cu.numel() < 2 or cu.dtype != _I32 or not cu.is_cuda or not cu.is_contiguous():
             raise AttambaError("cu must be a contiguous CUDA int32 [S + 1]")
-        self.S, self.T = cu.numel() - 1, int(T)
+        self.S, self.T, self.dev = cu.numel() - 1, int(T), cu.get_device()
         self.cu, self.slots, self.cont = cu, slots, cont
-        self._c = SeqsT(cu.data_ptr(), _dense(slots, cu, (self.S,), i32, "slots"),
-                        _dense(cont, cu, (self.S,), i32, "cont"), self.T, self.S)
+        self._c = SeqsT(cu.data_ptr(), _dense(slots, _I32, self.dev, (self.S,), "slots"),
+                        _dense(cont, _I32, self.dev, (self.S,), "cont"), self.T, self.S)
         self._ref = ctypes.byref(self._c)
 
-    def c_ref(self, like):
-        if self.cu.device != like.device:
-            raise AttambaError(f"the sequence table must be on {like.device}, got {self.cu.device}")
-        if self.T != like.shape[0]:
-            raise AttambaError(f"the sequence table is for {self.T} token rows, got {like.shape[0]}")
+    def c_ref(self, dev, T):
+        if self.dev != dev or self.T != T:
+            raise AttambaError(f"the sequence table is for {self.T} token rows on cuda:{self.dev}, got {T} on cuda:{dev}")
         return self._ref
 
 
-def _state(state, like, rows, dtype, name="state"):
-    """(device pointer, slots) of a contiguous [slots, rows, D] state; (None, 0) for None."""
-    if state is None:
-        return None, 0
-    n = state.shape[0] if state.dim() else 0
-    return _dense(state, like, (n, rows, like.shape[1]), dtype, name), n
-
-
 def _conv_args(x, w, bias, state, y):
-    _on_cuda(x, "x")
-    T, D = x.shape
-    if w.dim() != 2:
-        raise AttambaError("w must be [D, K]")
-    K = w.shape[1]
-    f32 = torch.float32
-    px, ldx = _rows(x, x, T, D, "x")
-    py, ldy = _rows(y, x, T, D, "y")
-    pst, n = _state(state, x, K - 1, x.dtype)
-    return (_dtype_code(x), px, ldx, _dense(w, x, (D, K), f32, "w"), _dense(bias, x, (D,), f32, "bias"), D, K,
-            pst, n, py, ldy)
+    code, dtype, dev, shape = _lead(x, "x")
+    D = shape[1]
+    K = w.shape[-1]
+    px, ldx = _rows(x, dtype, dev, shape, "x")
+    py, ldy = _rows(y, dtype, dev, shape, "y")
+    pst, n = _state(state, dtype, dev, K - 1, D)
+    return (dev, shape[0], (code, px, ldx, _dense(w, _F32, dev, (D, K), "w"), _dense(bias, _F32, dev, (D,), "bias"), D, K),
+            (pst, n, py, ldy))
 
 
 def causal_conv(x, w, bias, seqs, y, state=None, act=ACT_SILU, status=None, stream=None):
     """attamba_causal_conv: y [T, D] = act(bias + short causal depthwise convolution of x [T, D]) over the
     sequences of ``seqs``.  w [D, K] f32 (K 2 to 4), bias [D] f32 or None, state [slots, K - 1, D] or None."""
-    code, px, ldx, pw, pb, D, K, pst, n, py, ldy = _conv_args(x, w, bias, state, y)
-    _call(load().attamba_causal_conv, "attamba_causal_conv", x, status, stream, code, px, ldx, pw, pb, D, K, act,
-          seqs.c_ref(x), pst, n, py, ldy)
+    dev, T, head, tail = _conv_args(x, w, bias, state, y)
+    _call(load().attamba_causal_conv, "attamba_causal_conv", dev, stream,
+          (*head, act, seqs.c_ref(dev, T), *tail, _status(status, dev)))
 
 
 def conv_step(x, w, bias, state, y, slots=None, act=ACT_SILU, status=None, stream=None):
     """attamba_conv_step: causal_conv for one new token of each row of x [B, D]; ``slots`` [B] int32 names the
     rows' state rows (-1: a row that only fills the batch up; None: row b for row b)."""
-    code, px, ldx, pw, pb, D, K, pst, n, py, ldy = _conv_args(x, w, bias, state, y)
-    _call(load().attamba_conv_step, "attamba_conv_step", x, status, stream, code, px, ldx, pw, pb, D, K, act,
-          x.shape[0], _dense(slots, x, (x.shape[0],), torch.int32, "slots"), pst, n, py, ldy)
+    dev, B, head, tail = _conv_args(x, w, bias, state, y)
+    _call(load().attamba_conv_step, "attamba_conv_step", dev, stream,
+          (*head, act, B, _dense(slots, _I32, dev, (B,), "slots"), *tail, _status(status, dev)))
 
 
-def _scan_args(x, dt, bias, A, B, C, skip, z):
-    _on_cuda(x, "x")
-    T, D = x.shape
-    if A.dim() != 2:
-        raise AttambaError("A must be [D, N]")
-    N = A.shape[1]
-    f32 = torch.float32
-    return (_dtype_code(x), *_rows(x, x, T, D, "x"), *_rows(dt, x, T, D, "dt"), _dense(bias, x, (D,), f32, "bias"),
-            _dense(A, x, (D, N), f32, "A"), *_rows(B, x, T, N, "B"), *_rows(C, x, T, N, "C"),
-            _dense(skip, x, (D,), f32, "skip"), *_rows(z, x, T, D, "z"), D, N)
+def _scan_args(x, dt, bias, A, B, C, skip, z, state, y):
+    code, dtype, dev, shape = _lead(x, "x")
+    T, D = shape
+    N = A.shape[-1]
+    bc = (T, N)
+    pst, n = _state(state, _F32, dev, N, D)
+    return (dev, T, (code, *_rows(x, dtype, dev, shape, "x"), *_rows(dt, dtype, dev, shape, "dt"),
+                     _dense(bias, _F32, dev, (D,), "bias"), _dense(A, _F32, dev, (D, N), "A"),
+                     *_rows(B, dtype, dev, bc, "B"), *_rows(C, dtype, dev, bc, "C"),
+                     _dense(skip, _F32, dev, (D,), "skip"), *_rows(z, dtype, dev, shape, "z"), D, N),
+            (pst, n, *_rows(y, dtype, dev, shape, "y")))
 
 
 def selective_scan_workspace_size(T, D, N):
@@ -478,24 +485,19 @@ def selective_scan(x, dt, bias, A, B, C, seqs, y, skip=None, z=None, state=None,
     """attamba_selective_scan: the selective SSM over the sequences of ``seqs``.  x, dt, z, y [T, D]; B, C [T, N];
     A [D, N] f32; bias, skip [D] f32 or None; z None: no gate; state [slots, N, D] f32 or None; workspace:
     selective_scan_workspace_size(T, D, N) bytes (None where that is 0)."""
-    args = _scan_args(x, dt, bias, A, B, C, skip, z)
-    py, ldy = _rows(y, x, x.shape[0], x.shape[1], "y")
-    pst, n = _state(state, x, A.shape[1], torch.float32)
+    dev, T, head, tail = _scan_args(x, dt, bias, A, B, C, skip, z, state, y)
     pws, size = None, 0
     if workspace is not None:
-        size = workspace.numel() * workspace.element_size()
-        pws = _dense(workspace, x, workspace.shape, workspace.dtype, "workspace")
-    _call(load().attamba_selective_scan, "attamba_selective_scan", x, status, stream, *args, seqs.c_ref(x), pst, n, py,
-          ldy, pws, size)
+        pws, size = _dense(workspace, workspace.dtype, dev, workspace.shape, "workspace"), workspace.nbytes
+    _call(load().attamba_selective_scan, "attamba_selective_scan", dev, stream,
+          (*head, seqs.c_ref(dev, T), *tail, pws, size, _status(status, dev)))
 
 
 def scan_step(x, dt, bias, A, B, C, state, y, skip=None, z=None, slots=None, status=None, stream=None):
     """attamba_scan_step: selective_scan for one new token of each row of x [B, D]; ``slots`` as in conv_step."""
-    args = _scan_args(x, dt, bias, A, B, C, skip, z)
-    py, ldy = _rows(y, x, x.shape[0], x.shape[1], "y")
-    pst, n = _state(state, x, A.shape[1], torch.float32)
-    _call(load().attamba_scan_step, "attamba_scan_step", x, status, stream, *args, x.shape[0],
-          _dense(slots, x, (x.shape[0],), torch.int32, "slots"), pst, n, py, ldy)
+    dev, rows, head, tail = _scan_args(x, dt, bias, A, B, C, skip, z, state, y)
+    _call(load().attamba_scan_step, "attamba_scan_step", dev, stream,
+          (*head, rows, _dense(slots, _I32, dev, (rows,), "slots"), *tail, _status(status, dev)))
 
 
 def block_norm(y, res, res_out=None, h=None, w_post=None, w_pre=None, gate=None, gate_act=ACT_SILU, gate_first=False,
@@ -503,18 +505,22 @@ def block_norm(y, res, res_out=None, h=None, w_post=None, w_pre=None, gate=None,
     """attamba_block_norm: the norms after a block (w_post) and before the next (w_pre) with its gate, residual
     scale and sum: res_out = res + alpha scale norm(y) act(gate), h = norm(res_out).  Row tensors [M, D]; y or res
     may be None, and either output; the weights and scale are [D] f32."""
-    first = y if y is not None else res
-    if first is None:
+    lead = y if y is not None else res
+    if lead is None:
         raise AttambaError("block_norm needs y or res")
-    _on_cuda(first, "y" if y is not None else "res")
-    M, D = first.shape
-    f32 = torch.float32
-    typed = y if y is not None else h if h is not None else res         # the type of y, gate and h
-    rtyped = res if res is not None else res_out if res_out is not None else typed
-    args = (*_rows(y, first, M, D, "y"), *_rows(gate, first, M, D, "gate", typed.dtype), int(gate_act),
-            int(bool(gate_first)), _dense(w_post, first, (D,), f32, "w_post"),
-            *_rows(res, first, M, D, "res", rtyped.dtype), _dense(scale, first, (D,), f32, "scale"), float(alpha),
-            _dense(w_pre, first, (D,), f32, "w_pre"), float(eps), M, D,
-            *_rows(res_out, first, M, D, "res_out", rtyped.dtype), *_rows(h, first, M, D, "h", typed.dtype))
-    _call(load().attamba_block_norm, "attamba_block_norm", first, None, stream, _dtype_code(typed), _dtype_code(rtyped),
-          *args, with_status=False)
+    code, dtype, dev, shape = _lead(lead, "y" if y is not None else "res")
+    rcode, rtype = code, dtype
+    if y is None:                                   # only a norm: h's type is the block's, res keeps its own
+        if h is not None:
+            code, dtype = _dtype_code(h), h.dtype
+    else:
+        other = res if res is not None else res_out
+        if other is not None:
+            rtype = other.dtype
+            rcode = BF16 if rtype is _BF16 else _dtype_code(other)
+    w = (shape[1],)
+    _call(load().attamba_block_norm, "attamba_block_norm", dev, stream,
+          (code, rcode, *_rows(y, dtype, dev, shape, "y"), *_rows(gate, dtype, dev, shape, "gate"), gate_act,
+           1 if gate_first else 0, _dense(w_post, _F32, dev, w, "w_post"), *_rows(res, rtype, dev, shape, "res"),
+           _dense(scale, _F32, dev, w, "scale"), alpha, _dense(w_pre, _F32, dev, w, "w_pre"), eps, shape[0], shape[1],
+           *_rows(res_out, rtype, dev, shape, "res_out"), *_rows(h, dtype, dev, shape, "h")))

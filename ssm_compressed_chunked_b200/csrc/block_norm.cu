@@ -42,7 +42,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
 
 __device__ __forceinline__ float act_f(int act, float g) {
   if (act == ATTAMBA_ACT_LINEAR) return g;
-  const float s = __fdividef(1.f, 1.f + ex2(-g * kLog2e));
+  const float s = sigmoid_f(g);
   return act == ATTAMBA_ACT_SILU ? g * s : s;
 }
 

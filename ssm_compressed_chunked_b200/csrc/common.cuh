@@ -76,6 +76,22 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  float2 d;
+  asm("sub.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+
 // softplus(z) = log(1 + e^z) with u = e^z:  log2(1 + u) on the multi-function unit
 // when u >= 1/16 (its absolute error, about 2^-22, is then below 3e-6 of the
 // result), the series u - u^2/2 + u^3/3 - u^4/4 + u^5/5 below (truncation under
@@ -89,8 +105,20 @@ __device__ __forceinline__ float softplus_f(float z) {
   return z > 20.f ? z : v;
 }
 
-// silu(z) = z / (1 + e^-z); e^-z overflows to infinity for z < -88.7, the quotient is then -0
-__device__ __forceinline__ float silu_f(float z) { return __fdividef(z, 1.f + ex2(-z * kLog2e)); }
+// 1 / (1 + e^-z) and silu(z) = z / (1 + e^-z), with the hardware's reciprocal (2^-23 of the value).  e^-z overflows
+// to infinity for z < -88.7, its reciprocal is then 0.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sigmoid_f(float z) { return rcp(1.f + ex2(-z * kLog2e)); }
+__device__ __forceinline__ float silu_f(float z) { return z * sigmoid_f(z); }
+__device__ __forceinline__ float2 silu2(float2 z) {
+  const float2 e = mul2(z, make_float2(-kLog2e, -kLog2e));
+  const float2 d = add2(make_float2(ex2(e.x), ex2(e.y)), make_float2(1.f, 1.f));
+  return mul2(z, make_float2(rcp(d.x), rcp(d.y)));
+}
 
 // Number of entries of the ascending row p[0, n) that are below v, by all 32 lanes:
 // each round probes 32 evenly spaced entries and keeps the gap where the answer lies.
@@ -112,14 +140,46 @@ __device__ __forceinline__ int count_below_warp(const int32_t* p, int n, int v, 
 // Whether sequence (or batch row) s may use its state row: the slot lies in [0, n_slots) and no earlier
 // one has it.  By all 32 lanes; a wrong slot raises ATTAMBA_DEV_BAD_SEQS.  Returns the slot, or -1.
 __device__ __forceinline__ int state_slot_warp(const int32_t* slots, int s, int n_slots, int lane, int32_t* st) {
-  const int slot = slots ? slots[s] : s;
+  const int slot = slots ? __ldg(slots + s) : s;
   if (slot == -1) return -1;
   bool bad = slot < 0 || slot >= n_slots;
-  if (slots && !bad)
-    for (int i = lane; i < s; i += 32) bad |= slots[i] == slot;
+  if (slots && !bad) {
+#pragma unroll 8
+    for (int i = lane; i < s; i += 32) bad |= __ldg(slots + i) == slot;
+  }
   if (__any_sync(0xffffffffu, bad)) {
     if (lane == 0) raise_status(st, ATTAMBA_DEV_BAD_SEQS);
     return -1;
+  }
+  return slot;
+}
+
+// state_slot_warp for up to 32 batch rows first, first + stride, ... < rows at once: lane j gets row j's answer.  The
+// slots ahead of the rows are read once for all of them.
+__device__ __forceinline__ int state_slots_warp(const int32_t* slots, int first, int stride, int rows, int n_slots,
+                                                int lane, int32_t* st) {
+  const int64_t mine = first + (int64_t)lane * stride;
+  int slot = mine < rows ? (slots ? __ldg(slots + mine) : (int)mine) : -1;
+  bool bad = slot != -1 && (slot < 0 || slot >= n_slots);
+  if (slots) {
+    const int n = min(32, (rows - first + stride - 1) / stride);
+    const int last = first + (n - 1) * stride;   // slots[0, last) lie ahead of some row
+    for (int j = lane; j - lane < last; j += 128) {
+      int v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = j + 32 * u < last ? __ldg(slots + j + 32 * u) : -1;
+      for (int i = 0; i < n; ++i) {
+        const int s = __shfl_sync(0xffffffffu, slot, i), b = first + i * stride;
+        bool same = false;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) same |= v[u] == s && j + 32 * u < b;
+        if (__any_sync(0xffffffffu, same) && lane == i && slot != -1) bad = true;
+      }
+    }
+  }
+  if (bad) {
+    raise_status(st, ATTAMBA_DEV_BAD_SEQS);
+    slot = -1;
   }
   return slot;
 }
@@ -135,6 +195,14 @@ __device__ __forceinline__ void check_sequences_warp(const int32_t* cu, int S, i
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
+
+// asynchronous copies of 8 or 16 bytes, global to shared, and the thread's groups of them
+template <int BYTES> __device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");

@@ -72,22 +72,6 @@ constexpr float kP1 = 0.6932609677314758f;
 constexpr float kP2 = 0.2426111251115799f;
 constexpr float kP3 = 0.0551716685295105f;
 
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-  return d;
-}
-
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
-  float2 d;
-  asm("sub.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-  return d;
-}
-
 // 2^x for x in [-125, 0] on the FMA pipe (see the file comment)
 __device__ __forceinline__ float2 exp2_poly2(float2 x) {
   const float2 magic = make_float2(12582912.f, 12582912.f);  // 1.5 * 2^23: x + magic rounds x to an integer

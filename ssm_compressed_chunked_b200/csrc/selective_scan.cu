@@ -18,6 +18,8 @@
 // A tile that a sequence starts in takes the carried state in step 1 and keeps it for
 // step 3, whose last tile of that sequence replaces the state row.  One tile needs
 // step 3 alone.
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -25,7 +27,12 @@ namespace attamba {
 
 namespace {
 constexpr int kThreads = 128;
-constexpr int kStageTokens = 64;   // window of staged B and C rows
+constexpr int kWindowBytes = 16;   // a window's tokens times the element's size: 8 bf16 or 4 f32 tokens
+constexpr int kStages = 3;         // windows of x, dt and z in shared memory
+// 2^f = 1 + f (kE1 + f (kE2 + ...)) on [-1/2, 1/2]: least largest relative error, by linear programming over
+// the coefficients (9.2e-8; 1.7e-7 once the sums are rounded, unbiased near 0)
+constexpr float kE1 = 0.6931470036506653f, kE2 = 0.24022242426872253f, kE3 = 0.05550733953714371f,
+                kE4 = 0.009671511128544807f, kE5 = 0.0013264646986499429f;
 
 // CPT neighbouring channels of a token row
 template <typename T, int CPT> struct Row;
@@ -65,18 +72,47 @@ __host__ __device__ inline ScanWork scan_work(float* w, int tiles, int N, int D)
   return {w, w + n, w + 2 * n};
 }
 
+// 2^x for the x = dl a of a decay, on the FMA pipe: x = j + f with j the nearest integer, 2^f by a polynomial
+// with p(0) = 1, j added to the exponent field.  x is clamped at -126, where 2^x ends as the smallest normal
+// number (the hardware's instruction flushes what is below it to zero).
+__device__ __forceinline__ float2 decay_fma2(float2 dl, float2 a) {
+  const float2 magic = make_float2(12582912.f, 12582912.f);   // 1.5 * 2^23
+  const float2 x0 = mul2(dl, a);
+  const float2 x = make_float2(fmaxf(x0.x, -126.f), fmaxf(x0.y, -126.f));
+  const float2 t = add2(x, magic);
+  const float2 f = sub2(x, sub2(t, magic));
+  float2 q = fma2(f, make_float2(kE5, kE5), make_float2(kE4, kE4));
+  q = fma2(q, f, make_float2(kE3, kE3));
+  q = fma2(q, f, make_float2(kE2, kE2));
+  q = fma2(q, f, make_float2(kE1, kE1));
+  q = fma2(q, f, make_float2(1.f, 1.f));
+  return make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + __float_as_uint(q.x)),
+                     __uint_as_float((__float_as_uint(t.y) << 23) + __float_as_uint(q.y)));
+}
+
 // One block: kThreads / LPC * CPT channels of one tile.  LPC lanes share a channel, each with
 // NS / LPC of its states; FULL: the output pass.
-template <typename T, int CPT, int LPC, int NS, bool FULL, int MINB>
+template <typename T, int CPT, int LPC, int NS, bool FULL, int MINB, int POLY>
 __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p, int tile_len, int tiles) {
   using R = Row<T, CPT>;
   using raw = typename R::raw;
   constexpr int NPL = NS / LPC, NP = NPL / 2;
-  __shared__ __align__(16) float sBC[kStageTokens][2 * NS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int GT = LPC > 1 ? LPC : 2, TPL = GT / LPC;   // tokens of a group, and of them a lane's
+  constexpr int W = kWindowBytes / (int)sizeof(T) > GT ? kWindowBytes / (int)sizeof(T) : GT;   // tokens per window
+  constexpr int CB = kThreads / LPC * CPT;                // channels per block
+  constexpr int kArrays = FULL ? 3 : 2;                   // x, dt and z
+  constexpr int kBC = FULL ? 2 * NS : NS;
+  constexpr int kChunks = W * CB * (int)sizeof(T) / 16;   // 16-byte pieces of a window's array
+  constexpr int kBCPer = (W * kBC + kThreads - 1) / kThreads;
+  __shared__ __align__(16) T sRow[kStages][kArrays][W][CB];
+  __shared__ __align__(16) float sBC[2][W][kBC];
+  // The output pass after a state pass reads nothing the kernels between them and it write until it needs the
+  // carried state (below): its first loads overlap their end.
+  if (!FULL || tiles == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!FULL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int lane = threadIdx.x & 31;
-  const int groups = (p.D + kThreads / LPC * CPT - 1) / (kThreads / LPC * CPT);
+  const int groups = (p.D + CB - 1) / CB;
   const int tile = blockIdx.x / groups, group = blockIdx.x % groups;
   const int64_t t0 = (int64_t)tile * tile_len;
   const bool last_tile = tile == tiles - 1;
@@ -85,10 +121,78 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
   const int total = max(0, (int)min((int64_t)p.cu[p.S], p.T));
   const int t1 = (int)min(t0 + tile_len, (int64_t)total);
   const int D = p.D;
-  const int c0 = (group * kThreads + (int)threadIdx.x) / LPC * CPT;
-  const int n0 = (threadIdx.x % LPC) * NPL;
+  const int cb = group * CB;                              // the block's first channel
+  const int cl = threadIdx.x / LPC * CPT;                 // this thread's, in the block
+  const int c0 = cb + cl;
+  const int part = threadIdx.x % LPC;                     // and its share of the states
+  const int n0 = part * NPL;
   const bool active = c0 < D;
+  const bool gated = FULL && p.z != nullptr;
   const ScanWork ws = scan_work(p.work, tiles, NS, D);
+
+  // the tokens this block walks: its tile, or in the state pass the part of it that the state leaving it hangs on
+  int first = (int)min(t0, (int64_t)total);
+  int seq = 0;
+  if (!FULL) {
+    first = t1;
+    if (t0 + tile_len < total) {
+      seq = count_below_warp(p.cu, p.S, t1, lane) - 1;   // the last sequence that starts ahead of t1
+      if (seq >= 0 && p.cu[seq + 1] > t1) first = max(0, p.cu[seq]);
+    }
+    if (first >= t1) {   // no sequence reaches from this tile into the next
+      if (active && threadIdx.x % LPC == 0)
+        for (int c = 0; c < CPT; ++c) ws.sum[(size_t)tile * D + c0 + c] = -1.f;
+      return;
+    }
+  }
+  const bool starts = !FULL && first >= t0;
+  const int w0 = FULL ? first : (int)max((int64_t)first, t0);   // first token of window 0
+  const int windows = t1 > w0 ? (t1 - w0 + W - 1) / W : 0;
+
+  // window k: x, dt, z into stage k % kStages; B, C through registers, as fp32, into sBC[k % 2]
+  auto load_rows = [&](int k) {
+    if (k < windows) {
+      const int tw = w0 + k * W;
+#pragma unroll
+      for (int i = 0; i < (kChunks + kThreads - 1) / kThreads; ++i) {
+        const int e = threadIdx.x + i * kThreads;
+        const int row = e / (kChunks / W), col = e % (kChunks / W) * (16 / (int)sizeof(T));
+        const int tk = tw + row;
+        if (e < kChunks && tk < t1 && cb + col < D) {
+          T* dst = &sRow[k % kStages][0][row][col];
+          copy_async<16>(dst, static_cast<const T*>(p.x) + (int64_t)tk * p.ldx + cb + col);
+          copy_async<16>(dst + W * CB, static_cast<const T*>(p.dt) + (int64_t)tk * p.lddt + cb + col);
+          if (gated) copy_async<16>(dst + 2 * W * CB, static_cast<const T*>(p.z) + (int64_t)tk * p.ldz + cb + col);
+        }
+      }
+    }
+    copies_commit();   // a group per window, empty ones too: the wait counts groups
+  };
+  T bc[kBCPer];   // converted when stored: the conversion would wait for the load
+  auto load_bc = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < kBCPer; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      const int row = e / kBC, n = e % kBC;
+      const int tk = w0 + k * W + row;
+      bc[i] = T(0.f);
+      if (e < W * kBC && tk < t1 && k < windows)
+        bc[i] = n < NS ? static_cast<const T*>(p.Bm)[(int64_t)tk * p.ldb + n]
+                       : static_cast<const T*>(p.Cm)[(int64_t)tk * p.ldc + n - NS];
+    }
+  };
+  auto store_bc = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < kBCPer; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      if (e < W * kBC) (&sBC[k % 2][0][0])[e] = Elem<T>::to_f(bc[i]);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) load_rows(k);
+  load_bc(0);
+  store_bc(0);
+  load_bc(1);
 
   float2 a2[CPT][NP], h[CPT][NP];
   float bias[CPT], skip[CPT], sum[CPT];
@@ -105,13 +209,7 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
       h[c][q] = make_float2(0.f, 0.f);
     }
   }
-  const T* __restrict__ x = static_cast<const T*>(p.x) + c0;
-  const T* __restrict__ dt = static_cast<const T*>(p.dt) + c0;
-  const T* __restrict__ z = static_cast<const T*>(p.z) + c0;
-  const T* __restrict__ Bm = static_cast<const T*>(p.Bm);
-  const T* __restrict__ Cm = static_cast<const T*>(p.Cm);
   T* __restrict__ y = static_cast<T*>(p.y) + c0;
-  auto get = [&](const T* q, int t, int ld) { return __ldg(reinterpret_cast<const raw*>(q + (int64_t)t * ld)); };
 
   // state rows [NS, D]: this thread's CPT channels of its NPL states
   auto load_state = [&](const float* q) {
@@ -138,276 +236,476 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
       for (int q = 0; q < NP; ++q) h[c][q] = make_float2(0.f, 0.f);
   };
 
-  // tokens [a, b), all of one sequence; by the whole block
+  int window = -1;   // the window in shared memory that the walk has reached
+  // tokens [a, b), all of one sequence, next to those walked before; by the whole block
   auto walk = [&](int a, int b) {
-    const bool gated = FULL && p.z != nullptr;
-    auto tok = [&](int t) { return min(t, b - 1); };   // harmless reloads past the end
-    float dl[2][CPT], xv[2][CPT];
-    raw rx[2] = {}, rd[2] = {}, rz[2] = {}, rg[2] = {};
-    auto delta_of = [&](int j) {
-      float v[CPT];
-      R::unpack(rx[j], xv[j]);
-      R::unpack(rd[j], v);
+    for (int t = a; t < b;) {
+      const int k = (t - w0) / W;
+      if (k != window) {
+        window = k;
+        copies_wait<kStages - 2>();
+        __syncthreads();               // window k has arrived for all, window k - 1 has been read by all
+        load_rows(k + kStages - 1);
+        store_bc(k + 1);
+        load_bc(k + 2);
+      }
+      const int r0 = t - w0 - k * W, r1 = min(b - w0 - k * W, W);
+      const T* rx = &sRow[k % kStages][0][0][cl];
+      const float* rbc = &sBC[k % 2][0][n0];
+      // group of GT tokens: token j is prepared and finished by lane j % LPC of its channels' lanes
+      float xv[TPL][CPT], dl[TPL][CPT];
+      auto prepare = [&](int g) {
 #pragma unroll
-      for (int c = 0; c < CPT; ++c) dl[j][c] = softplus_f(v[c] + bias[c]);
-      rg[j] = rz[j];
-    };
-    auto fetch = [&](int j, int t) {
-      rx[j] = get(x, tok(t), p.ldx);
-      rd[j] = get(dt, tok(t), p.lddt);
-      if (gated) rz[j] = get(z, tok(t), p.ldz);
-    };
-    if (active) {
-      fetch(0, a);
-      fetch(1, a + 1);
-      delta_of(0);
-      delta_of(1);
-      fetch(0, a + 2);
-      fetch(1, a + 3);
-    }
-    auto step = [&](int t, int j, const float* bc) {
-      float out[CPT];
-      const float2* b2 = reinterpret_cast<const float2*>(bc + n0);
-      const float2* c2 = reinterpret_cast<const float2*>(bc + NS + n0);
+        for (int i = 0; i < TPL; ++i) {
+          const int r = min(g * GT + i * LPC + part, W - 1);   // past the window: not used
+          float v[CPT];
+          R::unpack(*reinterpret_cast<const raw*>(rx + r * CB), xv[i]);
+          R::unpack(*reinterpret_cast<const raw*>(rx + (W + r) * CB), v);
 #pragma unroll
-      for (int c = 0; c < CPT; ++c) {
-        const float2 dl2 = make_float2(dl[j][c], dl[j][c]);
-        const float dx = dl[j][c] * xv[j][c];
-        const float2 dx2 = make_float2(dx, dx);
-        float2 ya = make_float2(0.f, 0.f), yb = make_float2(0.f, 0.f);
+          for (int c = 0; c < CPT; ++c) dl[i][c] = softplus_f(v[c] + bias[c]);
+        }
+      };
+      auto group = [&](int g, auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;   // all GT tokens lie in [r0, r1)
+        float part_y[GT][CPT], dcur[TPL][CPT], xcur[TPL][CPT];
 #pragma unroll
-        for (int q = 0; q < NP; ++q) {
-          const float2 e = mul2(dl2, a2[c][q]);
-          h[c][q] = fma2(make_float2(ex2(e.x), ex2(e.y)), h[c][q], mul2(dx2, b2[q]));
-          if (FULL) {
-            if (q & 1) yb = fma2(c2[q], h[c][q], yb);
-            else ya = fma2(c2[q], h[c][q], ya);
+        for (int i = 0; i < TPL; ++i)
+#pragma unroll
+          for (int c = 0; c < CPT; ++c) {
+            dcur[i][c] = dl[i][c];
+            xcur[i][c] = xv[i][c];
+          }
+#pragma unroll
+        for (int j = 0; j < GT; ++j) {
+          const int r = g * GT + j;
+          const float2* b2 = reinterpret_cast<const float2*>(rbc + r * kBC);
+          const float2* c2 = reinterpret_cast<const float2*>(rbc + r * kBC + NS);
+          if (kWhole || (r >= r0 && r < r1)) {
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) {
+              float d = dcur[j / LPC][c], dx = dcur[j / LPC][c] * xcur[j / LPC][c];
+              if (LPC > 1) {
+                d = __shfl_sync(0xffffffffu, d, j % LPC, LPC);
+                dx = __shfl_sync(0xffffffffu, dx, j % LPC, LPC);
+              }
+              const float2 dl2 = make_float2(d, d), dx2 = make_float2(dx, dx);
+              float2 ya = make_float2(0.f, 0.f), yb = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int q = 0; q < NP; ++q) {
+                float2 a;
+                if (q < POLY) {
+                  a = decay_fma2(dl2, a2[c][q]);
+                } else {
+                  const float2 e = mul2(dl2, a2[c][q]);
+                  a = make_float2(ex2(e.x), ex2(e.y));
+                }
+                h[c][q] = fma2(a, h[c][q], mul2(dx2, b2[q]));
+                if (FULL) {
+                  if (q & 1) yb = fma2(c2[q], h[c][q], yb);
+                  else ya = q == 0 ? mul2(c2[q], h[c][q]) : fma2(c2[q], h[c][q], ya);
+                }
+              }
+              if (FULL) part_y[j][c] = NP > 1 ? (ya.x + ya.y) + (yb.x + yb.y) : ya.x + ya.y;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) part_y[j][c] = 0.f;
           }
         }
+        prepare(g + 1);
         if (FULL) {
-          float v = (ya.x + ya.y) + (yb.x + yb.y);
+          // sum over the lanes, halving the tokens a lane holds at each step: lane q ends with tokens j % LPC == q
 #pragma unroll
-          for (int m = 1; m < LPC; m *= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
-          out[c] = fmaf(skip[c], xv[j][c], v);
+          for (int m = LPC / 2; m > 0; m /= 2) {
+            const bool up = (part & m) != 0;
+#pragma unroll
+            for (int i = 0; i < GT / LPC; ++i)
+#pragma unroll
+              for (int u = 0; u < m; ++u)
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) {
+                  float& lo = part_y[i * LPC + u][c];
+                  const float hi = part_y[i * LPC + u + m][c];
+                  const float give = up ? lo : hi;
+                  lo = (up ? hi : lo) + __shfl_xor_sync(0xffffffffu, give, m);
+                }
+          }
+#pragma unroll
+          for (int i = 0; i < TPL; ++i) {
+            const int r = g * GT + i * LPC + part;
+            float out[CPT];
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) out[c] = fmaf(skip[c], xcur[i][c], part_y[i * LPC][c]);
+            if (gated) {
+              float z[CPT];
+              R::unpack(*reinterpret_cast<const raw*>(rx + (2 * W + r) * CB), z);
+              if (CPT == 2) {
+                const float2 g = silu2(make_float2(z[0], z[CPT - 1]));
+                out[0] *= g.x;
+                out[CPT - 1] *= g.y;
+              } else {
+                out[0] *= silu_f(z[0]);
+              }
+            }
+            if (active && (kWhole || (r >= r0 && r < r1)))
+              *reinterpret_cast<raw*>(y + (int64_t)(w0 + k * W + r) * p.ldy) = R::pack(out);
+          }
         } else {
-          sum[c] += dl[j][c];
-        }
-      }
-      if (FULL) {
-        if (gated) {
-          float g[CPT];
-          R::unpack(rg[j], g);
 #pragma unroll
-          for (int c = 0; c < CPT; ++c) out[c] *= silu_f(g[c]);
+          for (int i = 0; i < TPL; ++i) {
+            const int r = g * GT + i * LPC + part;
+            if (kWhole || (r >= r0 && r < r1)) {
+#pragma unroll
+              for (int c = 0; c < CPT; ++c) sum[c] += dcur[i][c];
+            }
+          }
         }
-        if (active && threadIdx.x % LPC == 0)
-          *reinterpret_cast<raw*>(y + (int64_t)t * p.ldy) = R::pack(out);
+      };
+      prepare(r0 / GT);
+#pragma unroll 1
+      for (int g = r0 / GT; g * GT < r1; ++g) {
+        if (g * GT >= r0 && (g + 1) * GT <= r1) group(g, std::true_type{});
+        else group(g, std::false_type{});
       }
-    };
-    for (int tb = a; tb < b; tb += kStageTokens) {
-      const int nt = min(kStageTokens, b - tb);
-      __syncthreads();
-      for (int e = threadIdx.x; e < nt * NS; e += kThreads) {
-        const int k = e / NS, n = e - k * NS;
-        sBC[k][n] = Elem<T>::to_f(Bm[(int64_t)(tb + k) * p.ldb + n]);
-        if (FULL) sBC[k][NS + n] = Elem<T>::to_f(Cm[(int64_t)(tb + k) * p.ldc + n]);
-      }
-      __syncthreads();
-      for (int k = 0; k < nt; k += 2) {
-        const int t = tb + k;
-        step(t, 0, &sBC[k][0]);
-        if (k + 1 < nt) step(t + 1, 1, &sBC[k + 1][0]);
-        if (active) {
-          delta_of(0);
-          delta_of(1);
-          fetch(0, t + 4);
-          fetch(1, t + 5);
-        }
-      }
+      t = w0 + k * W + r1;
     }
   };
 
   if (!FULL) {
-    // the sequence that tokens t1 - 1 and t1 both belong to, if any: only its state leaves the tile
-    float* sum_row = ws.sum + (size_t)tile * D;
-    int first = t1;
-    int s = 0;
-    if (t0 + tile_len < total) {
-      s = count_below_warp(p.cu, p.S, t1, lane) - 1;     // the last sequence that starts ahead of t1
-      if (s >= 0 && p.cu[s + 1] > t1) first = max(0, p.cu[s]);
-    }
-    if (first >= t1) {
-      if (active && threadIdx.x % LPC == 0)
-        for (int c = 0; c < CPT; ++c) sum_row[c0 + c] = -1.f;
-      return;
-    }
-    const bool starts = first >= t0;
     if (starts) {
-      const int slot = p.state ? state_slot_warp(p.slots, s, p.n_slots, lane, p.status) : -1;
-      if (slot >= 0 && p.cont && p.cont[s] != 0) {
+      const int slot = p.state ? state_slot_warp(p.slots, seq, p.n_slots, lane, p.status) : -1;
+      if (slot >= 0 && p.cont && p.cont[seq] != 0) {
         load_state(p.state + (size_t)slot * NS * D);
         store_state(ws.kept + (size_t)tile * NS * D);
       }
     }
-    walk((int)max((int64_t)first, t0), t1);
+    walk(w0, t1);
+#pragma unroll
+    for (int c = 0; c < CPT; ++c)
+#pragma unroll
+      for (int m = 1; m < LPC; m *= 2) sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], m);
     store_state(ws.end + (size_t)tile * NS * D);
     if (active && threadIdx.x % LPC == 0)
-      for (int c = 0; c < CPT; ++c) sum_row[c0 + c] = starts ? -1.f : sum[c];
+      for (int c = 0; c < CPT; ++c) ws.sum[(size_t)tile * D + c0 + c] = starts ? -1.f : sum[c];
     return;
   }
 
   // the first sequence that starts in this tile; the one before it may reach into the tile
   int s = count_below_warp(p.cu, p.S, (int)t0, lane);
+  int t = w0;
+  if (tiles > 1) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (s > 0 && tile > 0) {
     const int end = p.cu[s], b = min(end, t1);
     if (t0 < b) {
       load_state(ws.end + (size_t)(tile - 1) * NS * D);
       walk((int)t0, b);
+      t = b;
       if (end <= t1 && p.state) {
         const int slot = state_slot_warp(p.slots, s - 1, p.n_slots, lane, p.status);
         if (slot >= 0) store_state(p.state + (size_t)slot * NS * D);
       }
     }
   }
-  int t = (int)min(t0, (int64_t)total);
   for (; s < p.S; ++s) {
     const int cs = p.cu[s];
     if (cs >= t0 + tile_len && !last_tile) break;
-    const int first = min(max(cs, t), total);             // clamps act on a malformed cu only
-    const int end = min(max(p.cu[s + 1], first), total);
+    const int from = min(max(cs, t), total);              // clamps act on a malformed cu only
+    const int end = min(max(p.cu[s + 1], from), total);
     const int slot = p.state ? state_slot_warp(p.slots, s, p.n_slots, lane, p.status) : -1;
     zero_state();
     if (slot >= 0 && p.cont && p.cont[s] != 0)
       load_state(end > t1 ? ws.kept + (size_t)tile * NS * D : p.state + (size_t)slot * NS * D);
     const int b = min(end, t1);
-    if (first < b) walk(first, b);
+    if (from < b) walk(from, b);
     if (end <= t1 && slot >= 0) store_state(p.state + (size_t)slot * NS * D);
     t = max(t, b);
   }
+  copies_wait<0>();
 }
 
-// one thread per (n, d): end states of the tiles, in place
+// End states of the tiles, in place.  A block has 32 columns (n, d) and up to kJoinWarps runs of kJoin tiles: every
+// warp joins its run from zero, the runs' (decay, state) pairs meet in shared memory, and each thread walks
+// its run again from the state ahead of it.  The tiles' values stay in registers: one memory latency
+// for kJoin * kJoinWarps tiles.
+constexpr int kJoin = 8, kJoinWarps = 16;
 template <int NS>
-__global__ void __launch_bounds__(kThreads) scan_join_kernel(SelScanArgs p, int tiles) {
+__global__ void __launch_bounds__(32 * kJoinWarps) scan_join_kernel(SelScanArgs p, int tiles) {
+  __shared__ float sDecay[kJoinWarps][32], sEnd[kJoinWarps][32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int i = blockIdx.x * kThreads + threadIdx.x;   // n * D + d
-  if (i >= NS * p.D) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int i = blockIdx.x * 32 + lane;   // n * D + d; NS * D is a multiple of 32
   const int n = i / p.D, d = i - n * p.D;
   const ScanWork ws = scan_work(p.work, tiles, NS, p.D);
   const float a2 = p.A[(size_t)d * NS + n] * kLog2e;
-  float h = 0.f;
-  for (int k = 0; k + 1 < tiles; ++k) {
-    const float sum = ws.sum[(size_t)k * p.D + d];
-    float* e = ws.end + (size_t)k * NS * p.D + i;
-    h = sum < 0.f ? *e : fmaf(ex2(a2 * sum), h, *e);
-    *e = h;
+  const size_t ld = (size_t)NS * p.D;
+  float carry = 0.f;
+  for (int k0 = 0; k0 + 1 < tiles; k0 += kJoin * warps) {
+    const int k = k0 + warp * kJoin;
+    float sum[kJoin], e[kJoin];
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) {
+      const bool in = k + j + 1 < tiles;
+      sum[j] = in ? ws.sum[(size_t)(k + j) * p.D + d] : -1.f;
+      e[j] = in ? ws.end[(k + j) * ld + i] : 0.f;
+    }
+    float decay = 1.f, h = 0.f;
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) {
+      const bool fresh = sum[j] < 0.f;          // this tile's end state owes nothing to the tile ahead
+      sum[j] = fresh ? -1.f : ex2(a2 * sum[j]);   // from here on its decay
+      h = fresh ? e[j] : fmaf(sum[j], h, e[j]);
+      decay = fresh ? -1.f : (decay < 0.f ? decay : decay * sum[j]);
+    }
+    sDecay[warp][lane] = decay;
+    sEnd[warp][lane] = h;
+    __syncthreads();
+    h = carry;
+    for (int w = 0; w < warps; ++w) {
+      if (w == warp) carry = h;                 // the state ahead of this warp's run
+      h = sDecay[w][lane] < 0.f ? sEnd[w][lane] : fmaf(sDecay[w][lane], h, sEnd[w][lane]);
+    }
+    float s = carry;
+    carry = h;
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) {
+      s = sum[j] < 0.f ? e[j] : fmaf(sum[j], s, e[j]);
+      if (k + j + 1 < tiles) ws.end[(k + j) * ld + i] = s;
+    }
+    __syncthreads();                            // the pairs have been read
   }
 }
 
-// Single-token step.  A warp has 32 channels of one batch row: lane = (state quarter, 4 channels), so
-// its state accesses are 16 bytes a lane and a row of 128 bytes a quarter.
+// Single-token step.  A warp has 32 channels of a batch row: lane = (quarter of the states, 4 channels), so its
+// state accesses are 16 bytes a lane, 128 bytes of a state row a quarter.  A block walks several batch rows of its
+// 128 channels: A stays in registers, each thread copies its part of the next row's state into a ring of its own
+// (cp.async, no barrier) and loads the next row's inputs while it computes this one's.  Bound by reading and writing
+// the state: 251 rows x 2048 channels x 16 in 16.4 us (4.2 TB/s; a copy of these rows in the same pattern takes 14.9),
+// 256 x 4096 x 32 in 52 us (5.2 TB/s).  One row a block with everything in registers: 18.1 and 60.
+template <typename T> struct Four;
+template <> struct Four<float> {
+  using raw = float4;
+  static __device__ __forceinline__ void unpack(const raw& f, float (&v)[4]) { v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w; }
+};
+template <> struct Four<__nv_bfloat16> {
+  using raw = uint2;
+  static __device__ __forceinline__ void unpack(const raw& u, float (&v)[4]) {
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+};
+__device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+template <typename T> __device__ __forceinline__ typename Four<T>::raw get4(const void* p, int64_t at) {
+  return __ldg(reinterpret_cast<const typename Four<T>::raw*>(static_cast<const T*>(p) + at));
+}
+
+constexpr int kStepDepth = 2;                                                  // batch rows in a thread's ring
+constexpr int step_blocks(int NS) { return NS == 16 ? 6 : 3; }   // blocks on an SM: 7 or 8 spill and measured slower
 template <typename T, int NS>
-__global__ void __launch_bounds__(kThreads) scan_step_kernel(SelScanArgs p) {
+__global__ void __launch_bounds__(kThreads, step_blocks(NS)) scan_step_kernel(SelScanArgs p, int groups) {
   constexpr int NPL = NS / 4;
+  __shared__ __align__(16) float4 ring[kStepDepth][NPL][kThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.x;
-  const int slot = state_slot_warp(p.slots, b, p.n_slots, lane, p.status);
-  if (slot < 0) return;
-  const int c0 = ((int)blockIdx.y * (kThreads / 32) + warp) * 32 + (lane & 7) * 4;
+  const int c0 = (((int)blockIdx.x % groups) * (kThreads / 32) + warp) * 32 + (lane & 7) * 4;
   const int n0 = (lane >> 3) * NPL;
   const bool active = c0 < p.D;
-  float y[4] = {0.f, 0.f, 0.f, 0.f};
-  float x[4], v[4];
-  auto row4 = [&](const void* q, int ld, float (&o)[4]) {
-    const T* r = static_cast<const T*>(q) + (int64_t)b * ld + c0;
-    if (sizeof(T) == 4) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(r));
-      o[0] = f.x; o[1] = f.y; o[2] = f.z; o[3] = f.w;
-    } else {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(r));
-      o[0] = __uint_as_float(u.x << 16); o[1] = __uint_as_float(u.x & 0xffff0000u);
-      o[2] = __uint_as_float(u.y << 16); o[3] = __uint_as_float(u.y & 0xffff0000u);
-    }
+  const int first = blockIdx.x / groups, stride = gridDim.x / groups;   // this block's batch rows
+  const int rows = (int)p.T;
+  const size_t ld4 = (size_t)p.D / 4;
+  auto state_of = [&](int slot) {
+    return reinterpret_cast<float4*>(p.state + ((size_t)slot * NS + n0) * p.D + c0);
   };
-  if (active) {
-    float4* st = reinterpret_cast<float4*>(p.state + ((size_t)slot * NS + n0) * p.D + c0);
-    const size_t ld4 = (size_t)p.D / 4;
-    float4 h[NPL];
+  // a row's state on its way to the ring; a slot in range is safe to read before it is known to be good
+  auto fetch = [&](int i) {
+    const int b = first + i * stride;
+    if (b < rows && active) {
+      const int slot = p.slots ? __ldg(p.slots + b) : b;
+      if (slot >= 0 && slot < p.n_slots) {
+        const float4* st = state_of(slot);
 #pragma unroll
-    for (int n = 0; n < NPL; ++n) h[n] = st[n * ld4];
-    row4(p.x, p.ldx, x);
-    row4(p.dt, p.lddt, v);
-    float dl[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) dl[c] = softplus_f(v[c] + (p.bias ? __ldg(p.bias + c0 + c) : 0.f));
-    const T* Bm = static_cast<const T*>(p.Bm) + (int64_t)b * p.ldb + n0;
-    const T* Cm = static_cast<const T*>(p.Cm) + (int64_t)b * p.ldc + n0;
-#pragma unroll
-    for (int n = 0; n < NPL; ++n) {
-      const float Bn = Elem<T>::to_f(Bm[n]), Cn = Elem<T>::to_f(Cm[n]);
-      float* hn = reinterpret_cast<float*>(&h[n]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float a = __ldg(p.A + (size_t)(c0 + c) * NS + n0 + n) * kLog2e;
-        hn[c] = fmaf(ex2(dl[c] * a), hn[c], dl[c] * x[c] * Bn);
-        y[c] = fmaf(Cn, hn[c], y[c]);
+        for (int n = 0; n < NPL; ++n) copy_async<16>(&ring[i % kStepDepth][n][threadIdx.x], st + n * ld4);
       }
     }
+    copies_commit();
+  };
 #pragma unroll
-    for (int n = 0; n < NPL; ++n) st[n * ld4] = h[n];
-  }
+  for (int i = 0; i < kStepDepth - 1; ++i) fetch(i);
+  // This lane prepares (softplus) and finishes (skip, gate) one of the four channels.
+  const int oc = lane >> 3;
+  float2 A[NPL][2];   // A log2 e of state n0 + n: channels 0, 1 and 2, 3
+  float bias = 0.f, skip = 0.f;
+  if (active) {
+    if (p.bias) bias = __ldg(p.bias + c0 + oc);
+    if (p.skip) skip = __ldg(p.skip + c0 + oc);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    y[c] += __shfl_xor_sync(0xffffffffu, y[c], 8);
-    y[c] += __shfl_xor_sync(0xffffffffu, y[c], 16);
-  }
-  if (active && n0 == 0) {
-    if (p.skip) {
+    for (int n = 0; n < NPL; n += 4) {
+      float f[4][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) y[c] = fmaf(__ldg(p.skip + c0 + c), x[c], y[c]);
+      for (int c = 0; c < 4; ++c) Four<float>::unpack(get4<float>(p.A, (int64_t)(c0 + c) * NS + n0 + n), f[c]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        A[n + k][0] = make_float2(f[0][k] * kLog2e, f[1][k] * kLog2e);
+        A[n + k][1] = make_float2(f[2][k] * kLog2e, f[3][k] * kLog2e);
+      }
     }
-    if (p.z) {
-      row4(p.z, p.ldz, v);
+  }
+  // a row's inputs, loaded one row ahead of their use
+  using raw = typename Four<T>::raw;
+  raw rx = {}, rB[NPL / 4] = {}, rC[NPL / 4] = {};
+  T rdt = T(0.f), rz = T(0.f);
+  auto load = [&](int b) {
+    if (b >= rows || !active) return;
+    rx = get4<T>(p.x, (int64_t)b * p.ldx + c0);
+    rdt = static_cast<const T*>(p.dt)[(int64_t)b * p.lddt + c0 + oc];
+    if (p.z) rz = static_cast<const T*>(p.z)[(int64_t)b * p.ldz + c0 + oc];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) y[c] *= silu_f(v[c]);
+    for (int n = 0; n < NPL / 4; ++n) {
+      rB[n] = get4<T>(p.Bm, (int64_t)b * p.ldb + n0 + 4 * n);
+      rC[n] = get4<T>(p.Cm, (int64_t)b * p.ldc + n0 + 4 * n);
     }
-    T* o = static_cast<T*>(p.y) + (int64_t)b * p.ldy + c0;
-    if (sizeof(T) == 4) *reinterpret_cast<float4*>(o) = make_float4(y[0], y[1], y[2], y[3]);
-    else *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+  };
+  load(first);
+  int good = -1;   // lane j: the state row of batch row i + j (i a multiple of 32), while the first states are under way
+  for (int i = 0, b = first; b < rows; ++i, b += stride) {
+    if (i % 32 == 0) good = state_slots_warp(p.slots, b, stride, rows, p.n_slots, lane, p.status);
+    const int here = __shfl_sync(0xffffffffu, good, i % 32);
+    float x[4], Bn[NPL], Cn[NPL];
+    Four<T>::unpack(rx, x);
+#pragma unroll
+    for (int n = 0; n < NPL / 4; ++n) {
+      Four<T>::unpack(rB[n], reinterpret_cast<float(&)[4]>(Bn[4 * n]));
+      Four<T>::unpack(rC[n], reinterpret_cast<float(&)[4]>(Cn[4 * n]));
+    }
+    const float delta = softplus_f(Elem<T>::to_f(rdt) + bias), z = Elem<T>::to_f(rz);
+    load(b + stride);
+    copies_wait<kStepDepth - 2>();
+    fetch(i + kStepDepth - 1);
+    if (here < 0) continue;
+    float2 dl[2], dx[2], y[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      dl[k].x = __shfl_sync(0xffffffffu, delta, (lane & 7) + 16 * k);
+      dl[k].y = __shfl_sync(0xffffffffu, delta, (lane & 7) + 16 * k + 8);
+      dx[k] = mul2(dl[k], make_float2(x[2 * k], x[2 * k + 1]));
+    }
+    if (active) {
+      float4* st = state_of(here);
+      const float4* h4 = &ring[i % kStepDepth][0][threadIdx.x];
+#pragma unroll
+      for (int n = 0; n < NPL; ++n) {
+        const float4 old = h4[n * kThreads];
+        float2 h[2] = {make_float2(old.x, old.y), make_float2(old.z, old.w)};
+        const float2 B2 = make_float2(Bn[n], Bn[n]), C2 = make_float2(Cn[n], Cn[n]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 e = mul2(dl[k], A[n][k]);
+          h[k] = fma2(make_float2(ex2(e.x), ex2(e.y)), h[k], mul2(dx[k], B2));
+          y[k] = fma2(C2, h[k], y[k]);
+        }
+        st[n * ld4] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+      }
+    }
+    // sum over the four lanes of a channel group, halving the channels a lane holds: lane oc ends with channel oc
+    const bool up2 = (oc & 2) != 0, up1 = (oc & 1) != 0;
+    float2 s = up2 ? y[1] : y[0];
+    const float2 give = up2 ? y[0] : y[1];
+    s.x += __shfl_xor_sync(0xffffffffu, give.x, 16);
+    s.y += __shfl_xor_sync(0xffffffffu, give.y, 16);
+    float out = (up1 ? s.y : s.x) + __shfl_xor_sync(0xffffffffu, up1 ? s.x : s.y, 8);
+    const float xo = oc == 0 ? x[0] : oc == 1 ? x[1] : oc == 2 ? x[2] : x[3];
+    out = fmaf(skip, xo, out);
+    if (p.z) out *= silu_f(z);
+    if (active) store_elem(static_cast<T*>(p.y) + (int64_t)b * p.ldy + c0 + oc, out);
   }
 }
 
-// Tokens per tile.
-int scan_tile_len(int64_t T) { return 128; }
+// How a prompt batch is cut.  A variant is LPC lanes a channel (kThreads / LPC * CPT channels a block, `blocks`
+// of them on an SM); the tiles are as many as make one wave of blocks, so that none waits for a second.
+struct ScanPlan {
+  int lpc, tile_len, tiles, groups;
+};
+constexpr int kSMs = 148;
+constexpr int scan_cpt(int lpc, int NS) { return lpc <= 2 && NS == 16 ? 2 : 1; }
+constexpr int scan_blocks(int lpc) { return lpc == 1 ? 3 : lpc == 2 ? 4 : 5; }
+
+// One lane a channel costs the fewest instructions and is right where the SMs are full for long; two lanes halve the
+// work of a lone warp and double the warps, right up to about 2^27 tokens x channels x states (B200, bf16, us with 1 /
+// 2 lanes: T 16384 D 1024 N 16 189 / 205, 4096 x 2048 x 16 111 / 110, 16384 x 256 x 16 69 / 62, 2048 x 1024 x 16 42 / 36).
+// Four lanes need 32 channels a block instead of 256 or 128: for a D that would leave most of a block idle.
+// Up to kOneTile tokens, eight lanes a channel and a single tile: 61 x 1024 x 16 in 8.3 us and one launch, against 7.0 and two.
+constexpr int kOneTile = 64, kMinTile = 16;
+ScanPlan scan_plan(int64_t T, int32_t D, int32_t N) {
+  ScanPlan p{8, kOneTile, 1, 0};
+  auto width = [&](int lpc) { return kThreads / lpc * scan_cpt(lpc, N); };
+  if (T > kOneTile) {
+    const bool large = T * D * N > ((int64_t)1 << 27);
+    const int lanes[3] = {1, 2, 4};
+    const double cost[3] = {large ? 1.0 : 1.15, large ? 1.08 : 1.0, large ? 1.4 : 1.06};   // a full block's, measured
+    double best = 0;
+    for (int v = 0; v < 3; ++v) {
+      const double c = cost[v] * ((D + width(lanes[v]) - 1) / width(lanes[v]) * width(lanes[v])) / D;
+      if (v == 0 || c < best) {
+        best = c;
+        p.lpc = lanes[v];
+      }
+    }
+  }
+  p.groups = (D + width(p.lpc) - 1) / width(p.lpc);
+  if (T > kOneTile) {
+    const int64_t tiles = max(1, kSMs * scan_blocks(p.lpc) / p.groups);
+    const int64_t len = max((T + tiles - 1) / tiles, (int64_t)kMinTile);
+    p.tile_len = (int)((len + 7) / 8 * 8);
+    p.tiles = (int)((T + p.tile_len - 1) / p.tile_len);
+  }
+  return p;
+}
+
+template <typename T, int NS, int LPC>
+cudaError_t launch_tiles(const SelScanArgs& a, const ScanPlan& p, cudaStream_t s) {
+  constexpr int CPT = scan_cpt(LPC, NS), MINB = scan_blocks(LPC);
+  // state pairs whose decays run on the FMA pipe: one of 8 or two of 16 take 4% off (192 against 200 us, 332 against
+  // 347); more, or any with several lanes a channel, cost as much as they save
+  constexpr int POLY = LPC == 1 ? NS / 16 : 0;
+  const int64_t blocks = (int64_t)p.groups * p.tiles;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  if constexpr (LPC != 8) {   // eight lanes: one tile always
+    if (p.tiles > 1) {
+      cudaError_t e = launch_dependent(scan_tile_kernel<T, CPT, LPC, NS, false, MINB, POLY>,
+                                       dim3((unsigned)(blocks - p.groups)), kThreads, s, a, p.tile_len, p.tiles);
+      if (e != cudaSuccess) return e;
+      const int warps = min((p.tiles - 1 + kJoin - 1) / kJoin, kJoinWarps);
+      e = launch_dependent(scan_join_kernel<NS>, dim3(NS * a.D / 32), 32 * warps, s, a, p.tiles);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return launch_dependent(scan_tile_kernel<T, CPT, LPC, NS, true, MINB, POLY>, dim3((unsigned)blocks), kThreads, s, a,
+                          p.tile_len, p.tiles);
+}
 
 template <typename T, int NS>
 cudaError_t launch_scan(const SelScanArgs& a, cudaStream_t s) {
-  constexpr int CPT = NS == 16 ? 2 : 1;
-  const int len = scan_tile_len(a.T);
-  const int tiles = (int)((a.T + len - 1) / len);
-  const int64_t groups = (a.D + kThreads * CPT - 1) / (kThreads * CPT);
-  if (groups * tiles > 0x7fffffff) return cudaErrorInvalidValue;
-  cudaError_t e;
-  if (tiles > 1) {
-    e = launch_dependent(scan_tile_kernel<T, CPT, 1, NS, false, 3>, dim3((unsigned)(groups * (tiles - 1))), kThreads, s, a, len, tiles);
-    if (e != cudaSuccess) return e;
-    e = launch_dependent(scan_join_kernel<NS>, dim3((NS * a.D + kThreads - 1) / kThreads), kThreads, s, a, tiles);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_dependent(scan_tile_kernel<T, CPT, 1, NS, true, 3>, dim3((unsigned)(groups * tiles)), kThreads, s, a, len, tiles);
+  const ScanPlan p = scan_plan(a.T, a.D, NS);
+  if (p.lpc == 1) return launch_tiles<T, NS, 1>(a, p, s);
+  if (p.lpc == 2) return launch_tiles<T, NS, 2>(a, p, s);
+  if (p.lpc == 4) return launch_tiles<T, NS, 4>(a, p, s);
+  return launch_tiles<T, NS, 8>(a, p, s);
 }
 
 template <typename T, int NS>
 cudaError_t launch_step(const SelScanArgs& a, cudaStream_t s) {
-  return launch_dependent(scan_step_kernel<T, NS>, dim3((unsigned)a.T, (a.D + kThreads - 1) / kThreads), kThreads, s, a);
+  const int64_t groups = (a.D + kThreads - 1) / kThreads;
+  // one wave of blocks, each with the same number of batch rows but for the last
+  const int64_t wave = max((int64_t)1, kSMs * step_blocks(NS) / groups);
+  const int64_t each = (a.T + wave - 1) / wave;
+  const int64_t blocks = groups * ((a.T + each - 1) / each);
+  return launch_dependent(scan_step_kernel<T, NS>, dim3((unsigned)blocks), kThreads, s, a, (int)groups);
 }
 }  // namespace
 
 size_t selective_scan_workspace_bytes(int64_t T, int32_t D, int32_t N) {
-  const int len = scan_tile_len(T);
-  const int64_t tiles = (T + len - 1) / len;
-  return (size_t)(tiles - 1) * D * (2 * N + 1) * sizeof(float);
+  return (size_t)(scan_plan(T, D, N).tiles - 1) * D * (2 * N + 1) * sizeof(float);
 }
 
 cudaError_t launch_selective_scan(attamba_dtype_t dtype, const SelScanArgs& a, cudaStream_t s) {
