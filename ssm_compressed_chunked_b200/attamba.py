@@ -5,7 +5,8 @@ Every function here has the name of the C entry point it calls (without the
 contiguous and of the right dtype, passes their device pointers and the
 current CUDA stream, and raises ``AttambaError`` on a non-OK status.  All
 arithmetic happens in the library's kernels; there is no fallback path: if the
-library is missing or a tensor is on the CPU, the call raises.
+library is missing or a tensor is on the CPU, the call raises.  The SSM block's
+operators are marshalled the same way by a compiled module (see below).
 """
 
 import ctypes
@@ -345,75 +346,27 @@ def proj_gemm(X, W, outs, status=None, stream=None):
 # ---------------------------------------------------------------- the SSM block's operators
 # These take token rows [rows, cols] whose rows may be further apart than cols (column slices of a wide
 # projection), and run on the device of their tensors whichever device is current.  A decode step makes
-# several of these calls per layer and waits for the host, so the checks are few and flat: one pass over a
-# tensor's type, device, shape and strides, with the message made only when something is wrong.
+# several of these calls per layer and waits for the host, so their arguments are checked and passed by a compiled
+# module (csrc/binding.cpp, _binding.so): 4 us a call instead of 9 to 13 with the checks in Python.
 
-_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
-# the current stream's handle by device index; torch.cuda.current_stream builds a Stream object (2 us)
-_current_stream = torch._C._cuda_getCurrentRawStream
+_native_module = None
 
 
-def _rows(t, dtype, dev, shape, name):
-    """(device pointer, row stride) of a [rows, cols] tensor; (None, 0) for None."""
-    if t is None:
-        return None, 0
-    if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
-        ld, unit = t.stride()
-        if unit == 1 or shape[1] == 1:
-            return t.data_ptr(), ld if shape[0] > 1 else shape[1]
-    raise AttambaError(f"{name} must be {dtype} {list(shape)} on cuda:{dev} with its columns next to each other, got "
-                       f"{t.dtype} {list(t.shape)} on {t.device}, strides {t.stride()}")
-
-
-def _dense(t, dtype, dev, shape, name):
-    """Device pointer of a contiguous tensor; None for None."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    raise AttambaError(f"{name} must be a contiguous {dtype} {list(shape)} on cuda:{dev}, got {t.dtype} {list(t.shape)} "
-                       f"on {t.device}")
-
-
-def _lead(t, name):
-    """(dtype code, dtype, device index, shape) of the tensor the others are checked against."""
-    dev, dtype, shape = t.get_device(), t.dtype, t.shape
-    if dev < 0:
-        raise AttambaError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if len(shape) != 2 or shape[0] < 1:
-        raise AttambaError(f"{name} must be [rows >= 1, cols], got {list(shape)}")
-    return BF16 if dtype is _BF16 else _dtype_code(t), dtype, dev, shape
-
-
-def _state(state, dtype, dev, rows, cols):
-    """(device pointer, slots) of a contiguous [slots, rows, cols] state; (None, 0) for None."""
-    if state is None:
-        return None, 0
-    shape = state.shape
-    if len(shape) == 3 and shape[1] == rows and shape[2] == cols:
-        return _dense(state, dtype, dev, shape, "state"), shape[0]
-    raise AttambaError(f"state must be [slots, {rows}, {cols}], got {list(shape)}")
-
-
-def _call(fn, what, dev, stream, args):
-    """fn(*args, stream) with device ``dev`` current."""
-    if stream is None:
-        handle = _current_stream(dev)
-    elif stream.device.index == dev:
-        handle = stream.cuda_stream
-    else:
-        raise AttambaError(f"{what}: the stream is on {stream.device}, the tensors on cuda:{dev}")
-    if dev == torch.cuda.current_device():
-        st = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, handle)
-    if st != OK:
-        _check(st, what)
-
-
-def _status(status, dev):
-    return None if status is None else _dense(status, _I32, dev, (1,), "status")
+def _native():
+    """The marshalling module, holding the entry points of the loaded library."""
+    global _native_module
+    if _native_module is None:
+        L = load()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise AttambaError(f"_binding.so is missing or does not load ({e}): build it with python -m "
+                               "ssm_compressed_chunked_b200.build") from e
+        address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+        _binding.init(AttambaError, *(address(getattr(L, "attamba_" + k)) for k in (
+            "status_string", "last_error", "causal_conv", "conv_step", "selective_scan", "scan_step", "block_norm")))
+        _native_module = _binding
+    return _native_module
 
 
 class Seqs:
@@ -422,58 +375,30 @@ class Seqs:
     [S] non-zero where the sequence continues from its state row (None: none does)."""
 
     def __init__(self, cu, T, slots=None, cont=None):
-        if cu.dim() != 1 or cu.numel() < 2 or cu.dtype != _I32 or not cu.is_cuda or not cu.is_contiguous():
-            raise AttambaError("cu must be a contiguous CUDA int32 [S + 1]")
+        for name, t in (("cu", cu), ("slots", slots), ("cont", cont)):
+            if t is None and name != "cu":
+                continue
+            n = cu.numel() - (name != "cu")
+            if t.dim() != 1 or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n or \
+                    t.device != cu.device or cu.numel() < 2:
+                raise AttambaError(f"{name} must be a contiguous CUDA int32 [{'S + 1' if name == 'cu' else 'S'}] on one device")
         self.S, self.T, self.dev = cu.numel() - 1, int(T), cu.get_device()
         self.cu, self.slots, self.cont = cu, slots, cont
-        self._c = SeqsT(cu.data_ptr(), _dense(slots, _I32, self.dev, (self.S,), "slots"),
-                        _dense(cont, _I32, self.dev, (self.S,), "cont"), self.T, self.S)
-        self._ref = ctypes.byref(self._c)
-
-    def c_ref(self, dev, T):
-        if self.dev != dev or self.T != T:
-            raise AttambaError(f"the sequence table is for {self.T} token rows on cuda:{self.dev}, got {T} on cuda:{dev}")
-        return self._ref
-
-
-def _conv_args(x, w, bias, state, y):
-    code, dtype, dev, shape = _lead(x, "x")
-    D = shape[1]
-    K = w.shape[-1]
-    px, ldx = _rows(x, dtype, dev, shape, "x")
-    py, ldy = _rows(y, dtype, dev, shape, "y")
-    pst, n = _state(state, dtype, dev, K - 1, D)
-    return (dev, shape[0], (code, px, ldx, _dense(w, _F32, dev, (D, K), "w"), _dense(bias, _F32, dev, (D,), "bias"), D, K),
-            (pst, n, py, ldy))
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self._c = SeqsT(p(cu), p(slots), p(cont), self.T, self.S)
+        self.address = ctypes.addressof(self._c)
 
 
 def causal_conv(x, w, bias, seqs, y, state=None, act=ACT_SILU, status=None, stream=None):
     """attamba_causal_conv: y [T, D] = act(bias + short causal depthwise convolution of x [T, D]) over the
     sequences of ``seqs``.  w [D, K] f32 (K 2 to 4), bias [D] f32 or None, state [slots, K - 1, D] or None."""
-    dev, T, head, tail = _conv_args(x, w, bias, state, y)
-    _call(load().attamba_causal_conv, "attamba_causal_conv", dev, stream,
-          (*head, act, seqs.c_ref(dev, T), *tail, _status(status, dev)))
+    _native().causal_conv(x, w, bias, seqs.address, seqs.T, seqs.dev, y, state, act, status, stream)
 
 
 def conv_step(x, w, bias, state, y, slots=None, act=ACT_SILU, status=None, stream=None):
     """attamba_conv_step: causal_conv for one new token of each row of x [B, D]; ``slots`` [B] int32 names the
     rows' state rows (-1: a row that only fills the batch up; None: row b for row b)."""
-    dev, B, head, tail = _conv_args(x, w, bias, state, y)
-    _call(load().attamba_conv_step, "attamba_conv_step", dev, stream,
-          (*head, act, B, _dense(slots, _I32, dev, (B,), "slots"), *tail, _status(status, dev)))
-
-
-def _scan_args(x, dt, bias, A, B, C, skip, z, state, y):
-    code, dtype, dev, shape = _lead(x, "x")
-    T, D = shape
-    N = A.shape[-1]
-    bc = (T, N)
-    pst, n = _state(state, _F32, dev, N, D)
-    return (dev, T, (code, *_rows(x, dtype, dev, shape, "x"), *_rows(dt, dtype, dev, shape, "dt"),
-                     _dense(bias, _F32, dev, (D,), "bias"), _dense(A, _F32, dev, (D, N), "A"),
-                     *_rows(B, dtype, dev, bc, "B"), *_rows(C, dtype, dev, bc, "C"),
-                     _dense(skip, _F32, dev, (D,), "skip"), *_rows(z, dtype, dev, shape, "z"), D, N),
-            (pst, n, *_rows(y, dtype, dev, shape, "y")))
+    _native().conv_step(x, w, bias, state, y, slots, act, status, stream)
 
 
 def selective_scan_workspace_size(T, D, N):
@@ -485,19 +410,13 @@ def selective_scan(x, dt, bias, A, B, C, seqs, y, skip=None, z=None, state=None,
     """attamba_selective_scan: the selective SSM over the sequences of ``seqs``.  x, dt, z, y [T, D]; B, C [T, N];
     A [D, N] f32; bias, skip [D] f32 or None; z None: no gate; state [slots, N, D] f32 or None; workspace:
     selective_scan_workspace_size(T, D, N) bytes (None where that is 0)."""
-    dev, T, head, tail = _scan_args(x, dt, bias, A, B, C, skip, z, state, y)
-    pws, size = None, 0
-    if workspace is not None:
-        pws, size = _dense(workspace, workspace.dtype, dev, workspace.shape, "workspace"), workspace.nbytes
-    _call(load().attamba_selective_scan, "attamba_selective_scan", dev, stream,
-          (*head, seqs.c_ref(dev, T), *tail, pws, size, _status(status, dev)))
+    _native().selective_scan(x, dt, bias, A, B, C, y, skip, z, state, seqs.address, seqs.T, seqs.dev, workspace, status,
+                             stream)
 
 
 def scan_step(x, dt, bias, A, B, C, state, y, skip=None, z=None, slots=None, status=None, stream=None):
     """attamba_scan_step: selective_scan for one new token of each row of x [B, D]; ``slots`` as in conv_step."""
-    dev, rows, head, tail = _scan_args(x, dt, bias, A, B, C, skip, z, state, y)
-    _call(load().attamba_scan_step, "attamba_scan_step", dev, stream,
-          (*head, rows, _dense(slots, _I32, dev, (rows,), "slots"), *tail, _status(status, dev)))
+    _native().scan_step(x, dt, bias, A, B, C, y, skip, z, state, slots, status, stream)
 
 
 def block_norm(y, res, res_out=None, h=None, w_post=None, w_pre=None, gate=None, gate_act=ACT_SILU, gate_first=False,
@@ -505,22 +424,4 @@ def block_norm(y, res, res_out=None, h=None, w_post=None, w_pre=None, gate=None,
     """attamba_block_norm: the norms after a block (w_post) and before the next (w_pre) with its gate, residual
     scale and sum: res_out = res + alpha scale norm(y) act(gate), h = norm(res_out).  Row tensors [M, D]; y or res
     may be None, and either output; the weights and scale are [D] f32."""
-    lead = y if y is not None else res
-    if lead is None:
-        raise AttambaError("block_norm needs y or res")
-    code, dtype, dev, shape = _lead(lead, "y" if y is not None else "res")
-    rcode, rtype = code, dtype
-    if y is None:                                   # only a norm: h's type is the block's, res keeps its own
-        if h is not None:
-            code, dtype = _dtype_code(h), h.dtype
-    else:
-        other = res if res is not None else res_out
-        if other is not None:
-            rtype = other.dtype
-            rcode = BF16 if rtype is _BF16 else _dtype_code(other)
-    w = (shape[1],)
-    _call(load().attamba_block_norm, "attamba_block_norm", dev, stream,
-          (code, rcode, *_rows(y, dtype, dev, shape, "y"), *_rows(gate, dtype, dev, shape, "gate"), gate_act,
-           1 if gate_first else 0, _dense(w_post, _F32, dev, w, "w_post"), *_rows(res, rtype, dev, shape, "res"),
-           _dense(scale, _F32, dev, w, "scale"), alpha, _dense(w_pre, _F32, dev, w, "w_pre"), eps, shape[0], shape[1],
-           *_rows(res_out, rtype, dev, shape, "res_out"), *_rows(h, dtype, dev, shape, "h")))
+    _native().block_norm(y, res, res_out, h, w_post, w_pre, gate, gate_act, gate_first, scale, alpha, eps, stream)

@@ -1,4 +1,5 @@
-"""Build libattamba.so and libattamba_checked.so in-tree with nvcc for sm_100a.
+"""Build libattamba.so and libattamba_checked.so in-tree with nvcc for sm_100a, and the
+_binding module (argument marshalling for the SSM block's operators) with g++.
 
     python -m ssm_compressed_chunked_b200.build [--verbose]
 
@@ -13,6 +14,7 @@ access.  It is a debugging build, selected with ATTAMBA_LIBRARY=checked.
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libattamba.so")
 LIB_CHECKED = os.path.join(HERE, "libattamba_checked.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["abi.cu", "chunk_index.cu", "kv_ssm_scan.cu", "chunk_attn.cu", "decode.cu", "handoff.cu", "proj_gemm.cu", "causal_conv.cu",
            "selective_scan.cu", "block_norm.cu", "device.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -33,13 +36,26 @@ def _nvcc(out, extra, verbose):
     return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True), out
 
 
+def _gxx(out):
+    """The CPython module: torch's headers and libraries, no CUDA code."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), sysconfig.get_paths()["include"], INCLUDE]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [f"-I{d}" for d in inc] + \
+        [os.path.join(CSRC, "binding.cpp"), "-o", out + ".tmp", "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda",
+         "-ltorch_cpu", "-ltorch_python"]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True), out
+
+
 def build(verbose=False):
-    jobs = [_nvcc(LIB, [], verbose), _nvcc(LIB_CHECKED, ["-DATTAMBA_CHECKED"], verbose)]
+    jobs = [_nvcc(LIB, [], verbose), _nvcc(LIB_CHECKED, ["-DATTAMBA_CHECKED"], verbose), _gxx(BINDING)]
     for proc, out in jobs:
         so, se = proc.communicate()
         if proc.returncode != 0:
             sys.stderr.write(so + se)
-            raise RuntimeError(f"nvcc failed for {os.path.basename(out)}")
+            raise RuntimeError(f"the compiler failed for {os.path.basename(out)}")
         os.replace(out + ".tmp", out)
         if verbose:
             sys.stderr.write(se)

@@ -336,6 +336,46 @@ def test_malformed_offsets_are_reported_and_stay_inside(cu):
     assert one.item() == A.DEV_BAD_SEQS and two.item() == A.DEV_BAD_SEQS
 
 
+def test_the_binding_checks_types_shapes_strides_and_devices():
+    D, N, K = 64, 16, 4
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    f32 = torch.float32
+    ok = dict(x=z(4, D), w=z(D, K, dt=f32), bias=z(D, dt=f32), state=z(5, K - 1, D), y=z(4, D), slots=i32([0, 1, 2, 3]))
+    A.conv_step(**ok)
+    wide = z(4, 2 * D)
+    for key, bad in (("x", z(4, D, 1)), ("x", z(0, D)), ("x", z(4, D, dt=torch.float16)), ("x", z(4, D).cpu()), ("y", z(3, D)),
+                     ("y", z(4, D, dt=f32)), ("y", z(D, 4).t()), ("y", z(4, D).cpu()), ("w", z(D, K)), ("w", z(K, D, dt=f32).t()),
+                     ("w", z(D, K, dt=f32).cpu()), ("bias", z(D + 8, dt=f32)), ("bias", z(2 * D, dt=f32)[::2]),
+                     ("state", z(5, K, D)), ("state", z(5, K - 1, D, dt=f32)), ("state", z(5, D)), ("state", None),
+                     ("slots", i32([0, 1, 2])), ("slots", i32([0, 1, 2, 3]).long()), ("slots", [0, 1, 2, 3]), ("y", None),
+                     ("y", wide[:, 1:D + 1]), ("y", ok["x"]), ("status", z(2, dt=torch.int32)), ("stream", 7)):
+        with pytest.raises((A.AttambaError, AttributeError)):
+            A.conv_step(**{**ok, key: bad})
+    A.conv_step(**{**ok, "x": wide[:, :D], "y": wide[:, D:], "stream": torch.cuda.Stream()})
+    seqs = A.Seqs(i32([0, 4]), 4)
+    with pytest.raises(A.AttambaError, match="sequence table"):
+        A.causal_conv(z(5, D), ok["w"], None, seqs, z(5, D))
+    for bad in (i32([0]), i32([[0, 4]]), i32([0, 4]).long(), i32([0, 4]).cpu()):
+        with pytest.raises(A.AttambaError, match="cu must"):
+            A.Seqs(bad, 4)
+    with pytest.raises(A.AttambaError, match="slots must"):
+        A.Seqs(i32([0, 4]), 4, slots=i32([0, 1]))
+    with pytest.raises(A.AttambaError, match="res must"):
+        A.block_norm(z(4, D), z(5, D), z(4, D))
+    with pytest.raises(A.AttambaError, match="w_pre must"):
+        A.block_norm(z(4, D), z(4, D), z(4, D), z(4, D), w_pre=z(D))
+    with pytest.raises(A.AttambaError, match="invalid argument"):
+        A.block_norm(z(4, D), z(4, D), z(4, D), eps=-1.0)
+    with pytest.raises(TypeError):
+        A.block_norm(z(4, D), z(4, D), z(4, D), alpha="x")
+    big = scan_inputs(300, D, N, torch.bfloat16, seed=1)
+    g = {k: to_gpu(v) for k, v in big.items()}
+    with pytest.raises(A.AttambaError, match="workspace"):
+        A.selective_scan(*(g[k] for k in ("x", "dt", "bias", "A", "B", "C")), A.Seqs(i32([0, 300]), 300), z(300, D))
+    with pytest.raises(A.AttambaError, match="C must"):
+        A.scan_step(*(g[k] for k in ("x", "dt", "bias", "A", "B", "x")), z(300, N, D, dt=f32), z(300, D))
+
+
 def test_other_streams_and_captured_graphs():
     """The prompt and step operators on a side stream, captured into two graphs with a workspace each and replayed
     together, give what the eager calls gave, bit for bit."""
