@@ -345,7 +345,8 @@ attamba_status_t attamba_conv_step(attamba_dtype_t dtype, const void* x, int64_t
                                    const int32_t* slots, void* state, int32_t n_slots, void* y, int64_t ldy,
                                    int32_t* d_status, attamba_stream_t stream);
 
-/* Bytes of device workspace attamba_selective_scan needs for T token rows (0 for sizes out of range). */
+/* Bytes of device workspace attamba_selective_scan needs for T token rows (0 for sizes out of range).  It never
+ * falls as T grows: a workspace for the largest call serves the smaller ones. */
 size_t attamba_selective_scan_workspace_size(int64_t T, int32_t D, int32_t N);
 
 /* attamba_selective_scan -- the selective SSM over packed prompts, state carried over whole sequences.

@@ -636,25 +636,28 @@ constexpr int scan_blocks(int lpc) { return lpc == 1 ? 3 : lpc == 2 ? 4 : 5; }
 // Four lanes need 32 channels a block instead of 256 or 128: for a D that would leave most of a block idle.
 // Up to kOneTile tokens, eight lanes a channel and a single tile: 61 x 1024 x 16 in 8.3 us and one launch, against 7.0 and two.
 constexpr int kOneTile = 64, kMinTile = 16;
+int scan_width(int lpc, int32_t N) { return kThreads / lpc * scan_cpt(lpc, N); }   // channels a block
+int scan_groups(int lpc, int32_t D, int32_t N) { return (D + scan_width(lpc, N) - 1) / scan_width(lpc, N); }
+int64_t scan_wave(int lpc, int32_t D, int32_t N) { return max(1, kSMs * scan_blocks(lpc) / scan_groups(lpc, D, N)); }
+
 ScanPlan scan_plan(int64_t T, int32_t D, int32_t N) {
   ScanPlan p{8, kOneTile, 1, 0};
-  auto width = [&](int lpc) { return kThreads / lpc * scan_cpt(lpc, N); };
   if (T > kOneTile) {
     const bool large = T * D * N > ((int64_t)1 << 27);
     const int lanes[3] = {1, 2, 4};
     const double cost[3] = {large ? 1.0 : 1.15, large ? 1.08 : 1.0, large ? 1.4 : 1.06};   // a full block's, measured
     double best = 0;
     for (int v = 0; v < 3; ++v) {
-      const double c = cost[v] * ((D + width(lanes[v]) - 1) / width(lanes[v]) * width(lanes[v])) / D;
+      const double c = cost[v] * scan_groups(lanes[v], D, N) * scan_width(lanes[v], N) / D;
       if (v == 0 || c < best) {
         best = c;
         p.lpc = lanes[v];
       }
     }
   }
-  p.groups = (D + width(p.lpc) - 1) / width(p.lpc);
+  p.groups = scan_groups(p.lpc, D, N);
   if (T > kOneTile) {
-    const int64_t tiles = max(1, kSMs * scan_blocks(p.lpc) / p.groups);
+    const int64_t tiles = scan_wave(p.lpc, D, N);
     const int64_t len = max((T + tiles - 1) / tiles, (int64_t)kMinTile);
     p.tile_len = (int)((len + 7) / 8 * 8);
     p.tiles = (int)((T + p.tile_len - 1) / p.tile_len);
@@ -704,8 +707,13 @@ cudaError_t launch_step(const SelScanArgs& a, cudaStream_t s) {
 }
 }  // namespace
 
+// The most tiles that any variant cuts T rows or fewer into: it grows with T, so a workspace for the largest call
+// serves every smaller one.
 size_t selective_scan_workspace_bytes(int64_t T, int32_t D, int32_t N) {
-  return (size_t)(scan_plan(T, D, N).tiles - 1) * D * (2 * N + 1) * sizeof(float);
+  if (T <= kOneTile) return 0;
+  int64_t tiles = 1;
+  for (int lpc = 1; lpc <= 4; lpc *= 2) tiles = max(tiles, min(scan_wave(lpc, D, N), (T + kMinTile - 1) / kMinTile));
+  return (size_t)(tiles - 1) * D * (2 * N + 1) * sizeof(float);
 }
 
 cudaError_t launch_selective_scan(attamba_dtype_t dtype, const SelScanArgs& a, cudaStream_t s) {

@@ -5,6 +5,12 @@ and the whole layer with its projections around it.
 
     Layer:  x  --proj_gemm-->  q, dt_K, dt_V, B_K, C_K, B_V, C_V  --hot path-->  O  --proj_gemm-->  y = O W_O
 
+Beside it, the same selective SSM uncompressed, as a Mamba block's mixer, and the residual block around either:
+
+    SsmMixer:  h  --proj_gemm-->  x, z;  x  --causal_conv-->  u  --proj_gemm-->  dt, B, C;
+               selective_scan(u, dt, A, B, C, skip, z)  --proj_gemm-->  y
+    Block:     r  --block_norm-->  h  --mixer-->  y  --block_norm-->  r + alpha scale norm(y), and the next block's h
+
 Only buffer allocation happens here (torch, once); every step of the path runs
 in libattamba.so.
 """
@@ -198,3 +204,114 @@ class Layer:
         A.proj_gemm(pf.O.view(T, H * dh), self.W_O, [(self.y, 0)], self.status, stream)
         return self.y
 
+
+
+class SsmMixer:
+    """A Mamba block's mixer: the layer's selective SSM over whole sequences, with its short convolution, skip
+    and gate.
+
+    pith.science review of Attamba, "Assumptions & free parameters": the SSM is Mamba's selective SSM (Section
+    3.2, Eq. 3).  Here it is not chunked: its state runs through each sequence and is carried from call to call.
+    One GEMM gives the SSM input and its gate, the convolution (with SiLU) the scan's input u, a second GEMM the
+    step and B, C from u, the scan its gated output, a third GEMM y.
+
+    ``weights``: W_in [2 Di, D], W_x [Di + 2 N, Di] (rows dt, B, C), W_O [D, Di] bf16 in [out, in] layout; conv_w
+    [Di, K], A [Di, N] f32; conv_b, bias (of the step), skip [Di] f32 or absent.  D and Di are multiples of 64.
+    ``max_tokens`` bounds a call's token rows; the buffers are made once."""
+
+    def __init__(self, D, Di, N, K, weights, max_tokens, device="cuda", alloc=None):
+        bf, f32 = torch.bfloat16, torch.float32
+        shapes = {"W_in": ((2 * Di, D), bf), "W_x": ((Di + 2 * N, Di), bf), "W_O": ((D, Di), bf), "conv_w": ((Di, K), f32),
+                  "A": ((Di, N), f32), "conv_b": ((Di,), f32), "bias": ((Di,), f32), "skip": ((Di,), f32)}
+        for name, (shape, dt) in shapes.items():
+            w = weights.get(name)
+            if w is None and name in ("conv_b", "bias", "skip"):
+                continue
+            if w is None or tuple(w.shape) != shape or w.dtype != dt:
+                got = "none" if w is None else f"{w.dtype} {tuple(w.shape)}"
+                raise A.AttambaError(f"{name} must be {dt} {shape}, got {got}")
+        self.w = {k: (weights[k].contiguous() if weights.get(k) is not None else None) for k in shapes}
+        self.D, self.Di, self.N, self.K, self.max_tokens = D, Di, N, K, max_tokens
+        if alloc is None:
+            alloc = lambda shape, dt: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
+        widths = dict(x=Di, z=Di, u=Di, dt=Di, B=N, C=N, s=Di, y=D)
+        self.buf = {k: alloc((max_tokens, n), bf) for k, n in widths.items()}
+        self.workspace = torch.empty(A.selective_scan_workspace_size(max_tokens, Di, N), dtype=torch.uint8, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def new_state(self, slots):
+        """Carried states of ``slots`` sequences, all at zero: (convolution window, SSM state)."""
+        dev = self.w["A"].device
+        return (torch.zeros(slots, self.K - 1, self.Di, dtype=torch.bfloat16, device=dev),
+                torch.zeros(slots, self.N, self.Di, dtype=torch.float32, device=dev))
+
+    def _rows(self, T):
+        if not 1 <= T <= self.max_tokens:
+            raise A.AttambaError(f"{T} token rows; this mixer holds 1 to {self.max_tokens}")
+        return {k: b[:T] for k, b in self.buf.items()}
+
+    def _ends(self, h, b, stream):
+        """The input GEMM and a function for the two behind the convolution and behind the scan."""
+        A.proj_gemm(h, self.w["W_in"], [(b["x"], 0), (b["z"], self.Di)], self.status, stream)
+        Di, N = self.Di, self.N
+        return (lambda: A.proj_gemm(b["u"], self.w["W_x"], [(b["dt"], 0), (b["B"], Di), (b["C"], Di + N)], self.status, stream),
+                lambda: A.proj_gemm(b["s"], self.w["W_O"], [(b["y"], 0)], self.status, stream))
+
+    def forward(self, h, seqs, state=None, stream=None):
+        """h [T, D] bf16 over the sequences of ``seqs`` (attamba.Seqs) -> y [T, D] (the mixer's own buffer); ``state``
+        as from new_state, updated in place."""
+        b, w = self._rows(h.shape[0]), self.w
+        win, ssm = (None, None) if state is None else state
+        steps, out = self._ends(h, b, stream)
+        A.causal_conv(b["x"], w["conv_w"], w["conv_b"], seqs, b["u"], state=win, status=self.status, stream=stream)
+        steps()
+        A.selective_scan(b["u"], b["dt"], w["bias"], w["A"], b["B"], b["C"], seqs, b["s"], skip=w["skip"], z=b["z"],
+                         state=ssm, workspace=self.workspace, status=self.status, stream=stream)
+        out()
+        return b["y"]
+
+    def decode_step(self, state, h_t, slots=None, stream=None):
+        """One new token per sequence: h_t [B, D] bf16 -> y_t [B, D]; ``slots`` [B] int32 names the state rows."""
+        b, w = self._rows(h_t.shape[0]), self.w
+        win, ssm = state
+        steps, out = self._ends(h_t, b, stream)
+        A.conv_step(b["x"], w["conv_w"], w["conv_b"], win, b["u"], slots=slots, status=self.status, stream=stream)
+        steps()
+        A.scan_step(b["u"], b["dt"], w["bias"], w["A"], b["B"], b["C"], ssm, b["s"], skip=w["skip"], z=b["z"], slots=slots,
+                    status=self.status, stream=stream)
+        out()
+        return b["y"]
+
+
+class Block:
+    """A residual block around a mixer (``Layer`` or ``SsmMixer``): r + alpha scale norm(mixer(norm(r))).
+
+    ``w_pre`` [D] f32 is the norm ahead of the mixer, ``w_post`` (or None) the norm behind it, ``scale`` (or None)
+    a per-channel residual scale beside the number ``alpha``.  The residual stream r (bf16 or f32) is updated in
+    place.  The pass that adds y to r also makes the next block's input: hand its ``w_pre`` over as ``next_norm``
+    and give the returned h to the next block, whose own first norm then falls away."""
+
+    def __init__(self, mixer, w_pre, w_post=None, scale=None, alpha=1.0, eps=1e-5):
+        self.mixer, self.w_pre, self.w_post, self.scale, self.alpha, self.eps = mixer, w_pre, w_post, scale, alpha, eps
+
+    def _input(self, r, h, stream):
+        if h is None:
+            h = torch.empty(r.shape, dtype=torch.bfloat16, device=r.device)
+            A.block_norm(None, r, h=h, w_pre=self.w_pre, eps=self.eps, stream=stream)
+        return h
+
+    def _join(self, y, r, next_norm, stream):
+        h = None if next_norm is None else y      # the next input takes y's place
+        A.block_norm(y, r, res_out=r, h=h, w_post=self.w_post, w_pre=next_norm, scale=self.scale, alpha=self.alpha,
+                     eps=self.eps, stream=stream)
+        return r, h
+
+    def forward(self, r, *args, h=None, next_norm=None, stream=None, **kw):
+        """r [T, D] -> (r updated, the next block's h or None); the other arguments are the mixer's ``forward``'s."""
+        y = self.mixer.forward(self._input(r, h, stream), *args, stream=stream, **kw)
+        return self._join(y, r, next_norm, stream)
+
+    def decode_step(self, cache, r, *args, h=None, next_norm=None, stream=None, **kw):
+        """The same for one new token per sequence, through the mixer's ``decode_step``."""
+        y = self.mixer.decode_step(cache, self._input(r, h, stream), *args, stream=stream, **kw)
+        return self._join(y, r, next_norm, stream)

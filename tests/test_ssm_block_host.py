@@ -80,7 +80,9 @@ def test_selective_scan_says_how_much_workspace_it_needs():
     assert b"bytes of workspace" in A.load().attamba_last_error()
     size = A.selective_scan_workspace_size
     assert size(4096, 64, 16) > 0 and size(4096, 64, 32) > size(4096, 64, 16)
-    assert size(1 << 20, 64, 16) >= size(4096, 64, 16)
+    for D, N in ((64, 16), (264, 16), (1024, 16), (1024, 32), (8192, 32)):
+        sizes = [size(T, D, N) for T in [*range(1, 400), *range(400, 70000, 97), 1 << 20, 1 << 30]]
+        assert sizes == sorted(sizes) and sizes[0] == 0
     assert size(0, 64, 16) == 0 and size(4096, 60, 16) == 0 and size(4096, 64, 8) == 0 and size(1 << 31, 64, 16) == 0
 
 
