@@ -105,6 +105,23 @@ __device__ __forceinline__ float softplus_f(float z) {
   return z > 20.f ? z : v;
 }
 
+// softplus_f of a pair, the same steps two wide
+__device__ __forceinline__ float2 softplus2(float2 z) {
+  const float2 one = make_float2(1.f, 1.f);
+  const float2 e = mul2(z, make_float2(kLog2e, kLog2e));
+  const float2 u = make_float2(ex2(e.x), ex2(e.y)), w = add2(one, u);
+  float2 lg;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg.x) : "f"(w.x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg.y) : "f"(w.y));
+  lg = mul2(lg, make_float2(0.6931471805599453f, 0.6931471805599453f));
+  float2 s = fma2(u, make_float2(0.2f, 0.2f), make_float2(-0.25f, -0.25f));
+  s = fma2(u, s, make_float2(1.f / 3.f, 1.f / 3.f));
+  s = fma2(u, s, make_float2(-0.5f, -0.5f));
+  s = mul2(u, fma2(u, s, one));
+  const float a = u.x < 0.0625f ? s.x : lg.x, b = u.y < 0.0625f ? s.y : lg.y;
+  return make_float2(z.x > 20.f ? z.x : a, z.y > 20.f ? z.y : b);
+}
+
 // 1 / (1 + e^-z) and silu(z) = z / (1 + e^-z), with the hardware's reciprocal (2^-23 of the value).  e^-z overflows
 // to infinity for z < -88.7, its reciprocal is then 0.
 __device__ __forceinline__ float rcp(float x) {

@@ -27,8 +27,8 @@ namespace attamba {
 
 namespace {
 constexpr int kThreads = 128;
-constexpr int kWindowBytes = 16;   // a window's tokens times the element's size: 8 bf16 or 4 f32 tokens
-constexpr int kStages = 3;         // windows of x, dt and z in shared memory
+constexpr int kWindowBytes = 24;   // a window's tokens times the element's size: 12 bf16 or 6 f32 tokens
+constexpr int kStages = 2;         // windows of x, dt and z in shared memory
 // 2^f = 1 + f (kE1 + f (kE2 + ...)) on [-1/2, 1/2]: least largest relative error, by linear programming over
 // the coefficients (9.2e-8; 1.7e-7 once the sums are rounded, unbiased near 0)
 constexpr float kE1 = 0.6931470036506653f, kE2 = 0.24022242426872253f, kE3 = 0.05550733953714371f,
@@ -98,11 +98,10 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
   using raw = typename R::raw;
   constexpr int NPL = NS / LPC, NP = NPL / 2;
     constexpr int GT = LPC > 1 ? LPC : 2, TPL = GT / LPC;   // tokens of a group, and of them a lane's
-  constexpr int W = kWindowBytes / (int)sizeof(T) > GT ? kWindowBytes / (int)sizeof(T) : GT;   // tokens per window
+  constexpr int W = (kWindowBytes / (int)sizeof(T) + GT - 1) / GT * GT;   // tokens per window
   constexpr int CB = kThreads / LPC * CPT;                // channels per block
   constexpr int kArrays = FULL ? 3 : 2;                   // x, dt and z
   constexpr int kBC = FULL ? 2 * NS : NS;
-  constexpr int kChunks = W * CB * (int)sizeof(T) / 16;   // 16-byte pieces of a window's array
   constexpr int kBCPer = (W * kBC + kThreads - 1) / kThreads;
   __shared__ __align__(16) T sRow[kStages][kArrays][W][CB];
   __shared__ __align__(16) float sBC[2][W][kBC];
@@ -149,23 +148,29 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
   const int w0 = FULL ? first : (int)max((int64_t)first, t0);   // first token of window 0
   const int windows = t1 > w0 ? (t1 - w0 + W - 1) / W : 0;
 
-  // window k: x, dt, z into stage k % kStages; B, C through registers, as fp32, into sBC[k % 2]
+  // window k: x, dt, z into stage k % kStages; B, C through registers, as fp32, into sBC[k % 2].  A thread copies
+  // the same 16-byte column of every kRowStep-th row; its addresses move on by a window a call.
+  constexpr int kCols = CB * (int)sizeof(T) / 16, kRowStep = kThreads / kCols > 0 ? kThreads / kCols : 1;
+  static_assert(kCols <= kThreads, "a row of a window is at most a piece a thread");
+  const int crow = threadIdx.x / kCols, ccol = threadIdx.x % kCols * (16 / (int)sizeof(T));
+  const bool copies = cb + ccol < D;
+  const T* px = static_cast<const T*>(p.x) + (int64_t)(w0 + crow) * p.ldx + cb + ccol;
+  const T* pdt = static_cast<const T*>(p.dt) + (int64_t)(w0 + crow) * p.lddt + cb + ccol;
+  const T* pz = static_cast<const T*>(p.z) + (int64_t)(w0 + crow) * p.ldz + cb + ccol;
   auto load_rows = [&](int k) {
-    if (k < windows) {
-      const int tw = w0 + k * W;
+    const int left = t1 - w0 - k * W;   // tokens of the tile from this window on
+    T* dst = &sRow[k % kStages][0][crow][ccol];
 #pragma unroll
-      for (int i = 0; i < (kChunks + kThreads - 1) / kThreads; ++i) {
-        const int e = threadIdx.x + i * kThreads;
-        const int row = e / (kChunks / W), col = e % (kChunks / W) * (16 / (int)sizeof(T));
-        const int tk = tw + row;
-        if (e < kChunks && tk < t1 && cb + col < D) {
-          T* dst = &sRow[k % kStages][0][row][col];
-          copy_async<16>(dst, static_cast<const T*>(p.x) + (int64_t)tk * p.ldx + cb + col);
-          copy_async<16>(dst + W * CB, static_cast<const T*>(p.dt) + (int64_t)tk * p.lddt + cb + col);
-          if (gated) copy_async<16>(dst + 2 * W * CB, static_cast<const T*>(p.z) + (int64_t)tk * p.ldz + cb + col);
-        }
+    for (int r = 0; r < W; r += kRowStep) {
+      if ((W % kRowStep == 0 || crow + r < W) && crow + r < left && copies) {
+        copy_async<16>(dst + r * CB, px + (int64_t)r * p.ldx);
+        copy_async<16>(dst + (W + r) * CB, pdt + (int64_t)r * p.lddt);
+        if (gated) copy_async<16>(dst + (2 * W + r) * CB, pz + (int64_t)r * p.ldz);
       }
     }
+    px += (int64_t)W * p.ldx;
+    pdt += (int64_t)W * p.lddt;
+    pz += (int64_t)W * p.ldz;
     copies_commit();   // a group per window, empty ones too: the wait counts groups
   };
   T bc[kBCPer];   // converted when stored: the conversion would wait for the load
@@ -261,8 +266,13 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
           float v[CPT];
           R::unpack(*reinterpret_cast<const raw*>(rx + r * CB), xv[i]);
           R::unpack(*reinterpret_cast<const raw*>(rx + (W + r) * CB), v);
-#pragma unroll
-          for (int c = 0; c < CPT; ++c) dl[i][c] = softplus_f(v[c] + bias[c]);
+          if (CPT == 2) {
+            const float2 d = softplus2(make_float2(v[0] + bias[0], v[CPT - 1] + bias[CPT - 1]));
+            dl[i][0] = d.x;
+            dl[i][CPT - 1] = d.y;
+          } else {
+            dl[i][0] = softplus_f(v[0] + bias[0]);
+          }
         }
       };
       auto group = [&](int g, auto whole) {
@@ -305,7 +315,10 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
                   else ya = q == 0 ? mul2(c2[q], h[c][q]) : fma2(c2[q], h[c][q], ya);
                 }
               }
-              if (FULL) part_y[j][c] = NP > 1 ? (ya.x + ya.y) + (yb.x + yb.y) : ya.x + ya.y;
+              if (FULL) {
+                if (NP > 1) ya = add2(ya, yb);
+                part_y[j][c] = ya.x + ya.y;
+              }
             }
           } else {
 #pragma unroll
@@ -362,10 +375,15 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
         }
       };
       prepare(r0 / GT);
+      if (r0 == 0 && r1 == W) {
+#pragma unroll 2
+        for (int g = 0; g < W / GT; ++g) group(g, std::true_type{});
+      } else {
 #pragma unroll 1
-      for (int g = r0 / GT; g * GT < r1; ++g) {
-        if (g * GT >= r0 && (g + 1) * GT <= r1) group(g, std::true_type{});
-        else group(g, std::false_type{});
+        for (int g = r0 / GT; g * GT < r1; ++g) {
+          if (g * GT >= r0 && (g + 1) * GT <= r1) group(g, std::true_type{});
+          else group(g, std::false_type{});
+        }
       }
       t = w0 + k * W + r1;
     }
@@ -631,10 +649,11 @@ constexpr int scan_cpt(int lpc, int NS) { return lpc <= 2 && NS == 16 ? 2 : 1; }
 constexpr int scan_blocks(int lpc) { return lpc == 1 ? 3 : lpc == 2 ? 4 : 5; }
 
 // One lane a channel costs the fewest instructions and is right where the SMs are full for long; two lanes halve the
-// work of a lone warp and double the warps, right up to about 2^27 tokens x channels x states (B200, bf16, us with 1 /
-// 2 lanes: T 16384 D 1024 N 16 189 / 205, 4096 x 2048 x 16 111 / 110, 16384 x 256 x 16 69 / 62, 2048 x 1024 x 16 42 / 36).
-// Four lanes need 32 channels a block instead of 256 or 128: for a D that would leave most of a block idle.
-// Up to kOneTile tokens, eight lanes a channel and a single tile: 61 x 1024 x 16 in 8.3 us and one launch, against 7.0 and two.
+// work of a lone warp and double the warps, right below 2^27 tokens x channels x states (B200, bf16, us with 1 / 2 /
+// 4 lanes: 16384 x 1024 x 16 176 / 189 / 242, 8192 x 1024 x 16 97 / 100 / 124, 4096 x 1024 x 16 58 / 56 / 66,
+// 2048 x 1024 x 16 37 / 32 / 36, 512 x 1024 x 16 19 / 15 / 14). Four lanes need 32 channels a block instead of 256 or
+// 128: for a D that would leave most of a block idle.
+// Up to kOneTile tokens, eight lanes a channel and a single tile: 61 x 1024 x 16 in 6.9 us, one launch instead of three.
 constexpr int kOneTile = 64, kMinTile = 16;
 int scan_width(int lpc, int32_t N) { return kThreads / lpc * scan_cpt(lpc, N); }   // channels a block
 int scan_groups(int lpc, int32_t D, int32_t N) { return (D + scan_width(lpc, N) - 1) / scan_width(lpc, N); }
@@ -643,9 +662,9 @@ int64_t scan_wave(int lpc, int32_t D, int32_t N) { return max(1, kSMs * scan_blo
 ScanPlan scan_plan(int64_t T, int32_t D, int32_t N) {
   ScanPlan p{8, kOneTile, 1, 0};
   if (T > kOneTile) {
-    const bool large = T * D * N > ((int64_t)1 << 27);
+    const bool large = T * D * N >= ((int64_t)1 << 27);
     const int lanes[3] = {1, 2, 4};
-    const double cost[3] = {large ? 1.0 : 1.15, large ? 1.08 : 1.0, large ? 1.4 : 1.06};   // a full block's, measured
+    const double cost[3] = {large ? 1.0 : 1.15, large ? 1.06 : 1.0, large ? 1.37 : 1.1};   // a full block's, measured
     double best = 0;
     for (int v = 0; v < 3; ++v) {
       const double c = cost[v] * scan_groups(lanes[v], D, N) * scan_width(lanes[v], N) / D;
@@ -658,8 +677,7 @@ ScanPlan scan_plan(int64_t T, int32_t D, int32_t N) {
   p.groups = scan_groups(p.lpc, D, N);
   if (T > kOneTile) {
     const int64_t tiles = scan_wave(p.lpc, D, N);
-    const int64_t len = max((T + tiles - 1) / tiles, (int64_t)kMinTile);
-    p.tile_len = (int)((len + 7) / 8 * 8);
+    p.tile_len = (int)max((T + tiles - 1) / tiles, (int64_t)kMinTile);
     p.tiles = (int)((T + p.tile_len - 1) / p.tile_len);
   }
   return p;
@@ -668,8 +686,8 @@ ScanPlan scan_plan(int64_t T, int32_t D, int32_t N) {
 template <typename T, int NS, int LPC>
 cudaError_t launch_tiles(const SelScanArgs& a, const ScanPlan& p, cudaStream_t s) {
   constexpr int CPT = scan_cpt(LPC, NS), MINB = scan_blocks(LPC);
-  // state pairs whose decays run on the FMA pipe: one of 8 or two of 16 take 4% off (192 against 200 us, 332 against
-  // 347); more, or any with several lanes a channel, cost as much as they save
+  // state pairs whose decays run on the FMA pipe: one of 8 or two of 16 take 4% off (181 against 189 us, 319 against
+  // 331); more cost more than they save (2 of 8: 188), and so does any with several lanes a channel
   constexpr int POLY = LPC == 1 ? NS / 16 : 0;
   const int64_t blocks = (int64_t)p.groups * p.tiles;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
