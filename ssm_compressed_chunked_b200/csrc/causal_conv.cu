@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(32 * kConvWarps) causal_conv_kernel(ConvArgs p
   // of the thread's own ring, kDepth - 1 batches ahead of the arithmetic; a group of copies per batch, empty
   // ones too, so that the wait counts batches.
   auto walk = [&](int a, int b) {
+    if (!in_bounds(a >= 0 && b <= total && total <= p.T, p.status)) return;
     const T* src = x + (int64_t)a * p.ldx;
     auto fetch = [&](int g) {
 #pragma unroll
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(32 * kConvWarps) causal_conv_kernel(ConvArgs p
 #pragma unroll
       for (int k = 0; k < K - 1; ++k)
         *reinterpret_cast<raw*>(st + ((size_t)slot * (K - 1) + k) * p.D) =
-            b < end ? row(end - (K - 1) + k) : Pack<T>::pack(win[k]);
+            b < end && in_bounds(end - (K - 1) >= 0 && end <= total, p.status) ? row(end - (K - 1) + k) : Pack<T>::pack(win[k]);
     }
   }
 }

@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
   T* __restrict__ y = static_cast<T*>(p.y) + c0;
 
   // state rows [NS, D]: this thread's CPT channels of its NPL states
+  // (a state row lies in the state array: state_slot_warp; an end state and a kept one in the workspace: tile < tiles - 1)
   auto load_state = [&](const float* q) {
 #pragma unroll
     for (int n = 0; n < NPL; ++n)
@@ -244,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
   int window = -1;   // the window in shared memory that the walk has reached
   // tokens [a, b), all of one sequence, next to those walked before; by the whole block
   auto walk = [&](int a, int b) {
+    if (!in_bounds(a >= w0 && b <= t1 && t1 <= p.T, p.status)) return;   // the same for every thread
     for (int t = a; t < b;) {
       const int k = (t - w0) / W;
       if (k != window) {
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
   if (s > 0 && tile > 0) {
     const int end = p.cu[s], b = min(end, t1);
     if (t0 < b) {
-      load_state(ws.end + (size_t)(tile - 1) * NS * D);
+      if (in_bounds(tile - 1 < tiles - 1, p.status)) load_state(ws.end + (size_t)(tile - 1) * NS * D);
       walk((int)t0, b);
       t = b;
       if (end <= t1 && p.state) {
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
     const int end = min(max(p.cu[s + 1], from), total);
     const int slot = p.state ? state_slot_warp(p.slots, s, p.n_slots, lane, p.status) : -1;
     zero_state();
-    if (slot >= 0 && p.cont && p.cont[s] != 0)
+    if (slot >= 0 && p.cont && p.cont[s] != 0 && in_bounds(end <= t1 || tile < tiles - 1, p.status))
       load_state(end > t1 ? ws.kept + (size_t)tile * NS * D : p.state + (size_t)slot * NS * D);
     const int b = min(end, t1);
     if (from < b) walk(from, b);
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, step_blocks(NS)) scan_step_kernel(Se
     load(b + stride);
     copies_wait<kStepDepth - 2>();
     fetch(i + kStepDepth - 1);
-    if (here < 0) continue;
+    if (here < 0 || !in_bounds(here < p.n_slots, p.status)) continue;
     float2 dl[2], dx[2], y[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
