@@ -17,28 +17,39 @@
 namespace attamba {
 
 namespace {
-// 8 channels
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// 8 channels, as loaded and in fp32
+template <typename T> struct Eight;
+template <> struct Eight<float> {
+  struct raw {
+    float4 a, b;
+  };
+  static __device__ __forceinline__ raw get(const float* p) {
+    return {*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4)};
   }
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
+  static __device__ __forceinline__ void unpack(const raw& r, float (&v)[8]) {
+    v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w; v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+  }
+  static __device__ __forceinline__ void put(float* p, const float (&v)[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+template <> struct Eight<__nv_bfloat16> {
+  using raw = uint4;
+  static __device__ __forceinline__ raw get(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
+  static __device__ __forceinline__ void unpack(const raw& r, float (&v)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void put(__nv_bfloat16* p, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+};
 
 __device__ __forceinline__ float act_f(int act, float g) {
   if (act == ATTAMBA_ACT_LINEAR) return g;
@@ -71,24 +82,40 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kWarpRows : TPR) block_norm_k
   if (row >= p.M) return;   // whole warps only: a block of more threads has one row, below M
   const int id = threadIdx.x % TPR;
   const int D = p.D;
+  // A thread with one vector loads all of its row first: the two sums would otherwise each put a memory latency ahead of the next
+  // load (16384 x 2048, fp32 residual: 70.8 against 76.2 us).  With more vectors the registers that takes cost more
+  // blocks than it gives (4096 x 8192: 65 against 56 us), and gate and residual are loaded where they are used.
+  constexpr bool kFirst = VPT == 1;
   float v[VPT][8];
+  typename Eight<T>::raw g[VPT];
+  typename Eight<R>::raw r[VPT];
+  auto load_gate = [&](int k, int c) {
+    g[k] = {};
+    if (p.gate && c < D) g[k] = Eight<T>::get(static_cast<const T*>(p.gate) + row * p.ldg + c);
+  };
+  auto load_res = [&](int k, int c) {
+    r[k] = {};
+    if (p.res && c < D) r[k] = Eight<R>::get(static_cast<const R*>(p.res) + row * p.ldr + c);
+  };
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int c = (id + k * TPR) * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
-    if (p.y && c < D) load8(static_cast<const T*>(p.y) + row * p.ldy + c, v[k]);
+    if (p.y && c < D) Eight<T>::unpack(Eight<T>::get(static_cast<const T*>(p.y) + row * p.ldy + c), v[k]);
+    if (kFirst) {
+      load_gate(k, c);
+      load_res(k, c);
+    }
   }
   auto gate = [&]() {
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int c = (id + k * TPR) * 8;
-      if (c < D) {
-        float g[8];
-        load8(static_cast<const T*>(p.gate) + row * p.ldg + c, g);
+      float f[8];
+      if (!kFirst) load_gate(k, (id + k * TPR) * 8);
+      Eight<T>::unpack(g[k], f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] *= act_f(p.act, g[i]);
-      }
+      for (int i = 0; i < 8; ++i) v[k][i] *= act_f(p.act, f[i]);
     }
   };
   auto norm = [&](const float* w) {
@@ -103,7 +130,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kWarpRows : TPR) block_norm_k
       const int c = (id + k * TPR) * 8;
       if (c < D) {
         float f[8];
-        load8(w + c, f);
+        Eight<float>::unpack(Eight<float>::get(w + c), f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[k][i] *= rs * f[i];
       }
@@ -116,24 +143,24 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kWarpRows : TPR) block_norm_k
   for (int k = 0; k < VPT; ++k) {
     const int c = (id + k * TPR) * 8;
     if (c >= D) continue;
+    float f[8];
     if (p.scale) {
-      float f[8];
-      load8(p.scale + c, f);
+      Eight<float>::unpack(Eight<float>::get(p.scale + c), f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[k][i] *= f[i];
     }
-    float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (p.res) load8(static_cast<const R*>(p.res) + row * p.ldr + c, r);
+    if (!kFirst) load_res(k, c);
+    Eight<R>::unpack(r[k], f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[k][i] = p.y ? fmaf(p.alpha, v[k][i], r[i]) : r[i];
-    if (p.res_out) store8(static_cast<R*>(p.res_out) + row * p.ldro + c, v[k]);
+    for (int i = 0; i < 8; ++i) v[k][i] = p.y ? fmaf(p.alpha, v[k][i], f[i]) : f[i];
+    if (p.res_out) Eight<R>::put(static_cast<R*>(p.res_out) + row * p.ldro + c, v[k]);
   }
   if (p.h) {
     norm(p.w_pre);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int c = (id + k * TPR) * 8;
-      if (c < D) store8(static_cast<T*>(p.h) + row * p.ldh + c, v[k]);
+      if (c < D) Eight<T>::put(static_cast<T*>(p.h) + row * p.ldh + c, v[k]);
     }
   }
 }
@@ -146,14 +173,17 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
 
 template <typename T, typename R>
 cudaError_t launch_for(const NormArgs& a, cudaStream_t s) {
+  // threads a row and vectors a thread, measured (B200, GB/s of the copy's 6470): rows of 256 6050, 512 5510, 1024 6180,
+  // 2048 5550 (6640 with an fp32 residual), 4096 5270, 8192 4770, 16384 4080, 32768 3500; from 16384 on an SM holds too
+  // few rows to overlap one's sums with another's loads
   const int vecs = a.D / 8;
   if (vecs <= 32) return launch<T, R, 32, 1>(a, s);
-  if (vecs <= 64) return launch<T, R, 32, 2>(a, s);
+  if (vecs <= 64) return launch<T, R, 64, 1>(a, s);
   if (vecs <= 128) return launch<T, R, 128, 1>(a, s);
   if (vecs <= 256) return launch<T, R, 256, 1>(a, s);
   if (vecs <= 512) return launch<T, R, 256, 2>(a, s);
   if (vecs <= 1024) return launch<T, R, 512, 2>(a, s);
-  if (vecs <= 2048) return launch<T, R, 1024, 2>(a, s);
+  if (vecs <= 2048) return launch<T, R, 512, 4>(a, s);
   return launch<T, R, 1024, 4>(a, s);
 }
 }  // namespace

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
   using R = Row<T, CPT>;
   using raw = typename R::raw;
   constexpr int NPL = NS / LPC, NP = NPL / 2;
-    constexpr int GT = LPC > 1 ? LPC : 2, TPL = GT / LPC;   // tokens of a group, and of them a lane's
+  constexpr int GT = LPC > 1 ? LPC : 2, TPL = GT / LPC;   // tokens of a group, and of them a lane's
   constexpr int W = (kWindowBytes / (int)sizeof(T) + GT - 1) / GT * GT;   // tokens per window
   constexpr int CB = kThreads / LPC * CPT;                // channels per block
   constexpr int kArrays = FULL ? 3 : 2;                   // x, dt and z
