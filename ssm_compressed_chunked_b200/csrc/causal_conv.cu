@@ -9,8 +9,13 @@
 //
 // Mapping (B200).  Memory-bound: one read and one write of [T, D].  A thread owns
 // 4 channels and walks a run of tokens with the last K-1 inputs in registers, so
-// each input is read once but for the K-1 rows ahead of the run, and loads kAhead
-// rows together.  A warp has 128 neighbouring channels of one run.
+// each input is read once but for the K-1 rows ahead of the run.  A warp has 128
+// neighbouring channels, a block four warps of one run.  Rows come through a ring of
+// the thread's own in shared memory, 16 rows deep (cp.async, no barrier): held in
+// registers, the same rows in flight cost the blocks that hide the latency.
+// 32768 x 2048 bf16, K 4: 49 us, 5.4 TB/s (84% of the copy rate); rows loaded
+// into registers four or eight at a time 62, sixteen 74, one batch ahead 60-70.
+// SiLU takes two operations an element on the multi-function unit (65% busy).
 //
 // Ownership.  The run that holds a sequence's first token (or an empty sequence's
 // place) also computes that sequence's first K-1 tokens when they pass the run's

@@ -17,7 +17,23 @@
 //   3. scan_tile<output pass> per tile: from the end state of the tile before it.
 // A tile that a sequence starts in takes the carried state in step 1 and keeps it for
 // step 3, whose last tile of that sequence replaces the state row.  One tile needs
-// step 3 alone.
+// step 3 alone.  Steps 2 and 3 are programmatic dependents: their blocks are placed and
+// step 3's first windows loaded while the step before drains.
+//
+// Mapping (B200).  A block has the channels of 128 / LPC * CPT threads and walks its tile
+// token by token, the state and A log2 e in registers as f32x2 pairs over n.  x, dt and z
+// come in windows of 12 bf16 rows by cp.async, one window ahead; B and C, the same for
+// all channels, are staged as fp32 and read as broadcast 16-byte loads.  The loop is
+// independent of the sequences: a window is walked in runs that end where one does.
+//
+// What bounds it: the exponentials.  Both passes take T D N of them, on a unit that does
+// 16 a clock and SM, beside 4 (output) or 3 (state) half-rate f32x2 operations a pair: at
+// 16384 x 1024 x 16 (bf16, gated) that is 60 + 67 us at 1.9 GHz, and the call takes 176
+// (0.77 TB/s of 6.47).  The unit is 82% busy in the state pass, 69% in the output pass,
+// the issue slots 43 and 46%; three warps a scheduler is what the registers hold.  Measured and not kept: one channel a thread and five to seven blocks on an SM
+// (196-221 us), two channels at four blocks (194), three quarters of the window (186),
+// all groups of a window unrolled (185), the short batches' tiles as a cluster that exchanges
+// states through distributed shared memory (61 tokens 9.9 us against 6.9 in a single tile).
 #include <type_traits>
 
 #include "common.cuh"
@@ -655,8 +671,10 @@ constexpr int scan_blocks(int lpc) { return lpc == 1 ? 3 : lpc == 2 ? 4 : 5; }
 // 4 lanes: 16384 x 1024 x 16 176 / 189 / 242, 8192 x 1024 x 16 97 / 100 / 124, 4096 x 1024 x 16 58 / 56 / 66,
 // 2048 x 1024 x 16 37 / 32 / 36, 512 x 1024 x 16 19 / 15 / 14). Four lanes need 32 channels a block instead of 256 or
 // 128: for a D that would leave most of a block idle.
-// Up to kOneTile tokens, eight lanes a channel and a single tile: 61 x 1024 x 16 in 6.9 us, one launch instead of three.
-constexpr int kOneTile = 64, kMinTile = 16;
+// Up to kOneTile tokens, eight lanes a channel and a single tile, one launch instead of three (us, single against three:
+// 17 x 1024 x 16 4.2 / 11.6, 61 tokens 6.9 / 11.6, 96 8.6 / 11.9, 190 15.3 / 12.2; 128 x 4096 x 16 12.9 / 18.2,
+// 128 x 16384 x 16 29.6 / 38.3).
+constexpr int kOneTile = 128, kMinTile = 16;
 int scan_width(int lpc, int32_t N) { return kThreads / lpc * scan_cpt(lpc, N); }   // channels a block
 int scan_groups(int lpc, int32_t D, int32_t N) { return (D + scan_width(lpc, N) - 1) / scan_width(lpc, N); }
 int64_t scan_wave(int lpc, int32_t D, int32_t N) { return max(1, kSMs * scan_blocks(lpc) / scan_groups(lpc, D, N)); }
