@@ -314,9 +314,10 @@ typedef struct {
   const int32_t* cu;    /* [S + 1] first token of each sequence, cu[0] = 0, cu[S] <= T */
   const int32_t* slots; /* nullable [S] state row of each sequence, -1: none (it starts from zero and keeps
                            nothing); NULL: sequence s has row s */
-  const int32_t* cont;  /* nullable [S] nonzero: the sequence continues from its state row; NULL: none does */
+  const int32_t* cont;  /* nullable [S] nonzero: the sequence continues from its state row (a call without a state
+                           starts every sequence from zero); NULL: none does */
   int64_t T;            /* rows of the token arrays, 1 <= T < 2^31 - 65536 */
-  int32_t S;            /* sequences, 1 <= S <= 2^24 */
+  int32_t S;            /* sequences, 1 <= S <= 2^20, with slots <= 8192 */
 } attamba_seqs_t;
 
 /* Activation of a convolution or a gate. */
@@ -338,7 +339,8 @@ attamba_status_t attamba_causal_conv(attamba_dtype_t dtype, const void* x, int64
 
 /* attamba_conv_step -- attamba_causal_conv for one new token of each of B sequences that continue.
  *   x, y   [B, D], row strides ldx, ldy;  slots nullable [B]: -1 marks a row that only fills the
- *          batch up (its y is left as it is); NULL: row b has state row b.
+ *          batch up (its y is left as it is); NULL: row b has state row b.  B <= 2^20, with slots
+ *          <= 8192 (more: several calls).
  * A slot out of range or named by an earlier row raises ATTAMBA_DEV_BAD_SEQS; that row is skipped. */
 attamba_status_t attamba_conv_step(attamba_dtype_t dtype, const void* x, int64_t ldx, const float* w,
                                    const float* bias, int32_t D, int32_t K, attamba_act_t act, int32_t B,
@@ -369,7 +371,8 @@ attamba_status_t attamba_selective_scan(attamba_dtype_t dtype, const void* x, in
                                         size_t workspace_bytes, int32_t* d_status, attamba_stream_t stream);
 
 /* attamba_scan_step -- attamba_selective_scan for one new token of each of `rows` sequences that continue.
- *   x, dt, z, y [rows, D];  B, C [rows, N];  slots as in attamba_conv_step. */
+ *   x, dt, z, y [rows, D];  B, C [rows, N];  slots and the limit on
+ *   rows as in attamba_conv_step. */
 attamba_status_t attamba_scan_step(attamba_dtype_t dtype, const void* x, int64_t ldx, const void* dt, int64_t lddt,
                                    const float* bias, const float* A, const void* B, int64_t ldb, const void* C,
                                    int64_t ldc, const float* skip, const void* z, int64_t ldz, int32_t D, int32_t N,

@@ -347,7 +347,8 @@ struct Rows {
   const char* name;
 };
 bool ok_rows(const Rows& r) {
-  return aligned16(r.p) && r.ld >= r.cols && r.ld < ((int64_t)1 << 31) && (r.ld * r.es) % 16 == 0;
+  return aligned16(r.p) && r.ld >= r.cols && r.ld < ((int64_t)1 << 31) && (r.ld * r.es) % 16 == 0 &&
+         r.rows <= ((int64_t)1 << 56) / (r.ld * r.es);
 }
 // whether two row sets share a byte: column windows of one wide array (same stride) do not
 bool overlap(const Rows& a, const Rows& b) {
@@ -379,10 +380,19 @@ attamba_status_t check_rows(const Rows* r, int n, const char* what) {
 int elem_size(attamba_dtype_t d) { return d == ATTAMBA_BF16 ? 2 : 4; }
 constexpr int64_t kMaxSeqTokens = ((int64_t)1 << 31) - 65536;   // token positions plus a tile stay int32
 constexpr int32_t kMaxChannels = 1 << 20;
-constexpr int32_t kMaxRows = 1 << 24;                           // sequences or batch rows of one call
+constexpr int32_t kMaxRows = 1 << 20;                           // sequences or batch rows of one call
+// with a slot map: every row's slot is looked for among the ones ahead of it, which grows with the square: at 8192 rows it
+// takes a quarter of a decode step (D 1024, N 16: 234 us, 180 without a map), and most of a prompt batch of that many
+constexpr int32_t kMaxSlots = 8192;
+bool too_many(const int32_t* slots, int32_t rows, const char* what) {
+  if (rows <= (slots ? kMaxSlots : kMaxRows)) return false;
+  snprintf(g_err, sizeof(g_err), "%s: %d sequences in one call, at most %d%s", what, rows, slots ? kMaxSlots : kMaxRows,
+           slots ? " with slots" : "");
+  return true;
+}
 bool ok_channels(int32_t D) { return D >= 8 && D % 8 == 0 && D <= kMaxChannels; }
 bool ok_seqs(const attamba_seqs_t* q) {
-  return q && q->cu && q->T >= 1 && q->T < kMaxSeqTokens && q->S >= 1 && q->S <= kMaxRows;
+  return q && q->cu && q->T >= 1 && q->T < kMaxSeqTokens && q->S >= 1;
 }
 
 attamba_status_t conv_entry(attamba_dtype_t dtype, attamba::ConvArgs& a, int64_t ldx, int64_t ldy, int32_t K,
@@ -433,6 +443,7 @@ attamba_status_t attamba_causal_conv(attamba_dtype_t dtype, const void* x, int64
                                      const attamba_seqs_t* seqs, void* state, int32_t n_slots, void* y,
                                      int64_t ldy, int32_t* d_status, attamba_stream_t stream) {
   if (!ok_seqs(seqs)) return ATTAMBA_ERR_INVALID_ARG;
+  if (too_many(seqs->slots, seqs->S, "attamba_causal_conv")) return ATTAMBA_ERR_UNSUPPORTED;
   attamba::ConvArgs a{};
   a.x = x; a.w = w; a.bias = bias; a.state = state; a.y = y;
   a.cu = seqs->cu; a.slots = seqs->slots; a.cont = seqs->cont;
@@ -444,7 +455,8 @@ attamba_status_t attamba_conv_step(attamba_dtype_t dtype, const void* x, int64_t
                                    const float* bias, int32_t D, int32_t K, attamba_act_t act, int32_t B,
                                    const int32_t* slots, void* state, int32_t n_slots, void* y, int64_t ldy,
                                    int32_t* d_status, attamba_stream_t stream) {
-  if (B < 1 || B > kMaxRows || !state) return ATTAMBA_ERR_INVALID_ARG;
+  if (B < 1 || !state) return ATTAMBA_ERR_INVALID_ARG;
+  if (too_many(slots, B, "attamba_conv_step")) return ATTAMBA_ERR_UNSUPPORTED;
   attamba::ConvArgs a{};
   a.x = x; a.w = w; a.bias = bias; a.state = state; a.y = y; a.slots = slots;
   a.T = B; a.D = D; a.n_slots = n_slots; a.status = d_status;
@@ -463,6 +475,7 @@ attamba_status_t attamba_selective_scan(attamba_dtype_t dtype, const void* x, in
                                         int32_t n_slots, void* y, int64_t ldy, void* workspace,
                                         size_t workspace_bytes, int32_t* d_status, attamba_stream_t stream) {
   if (!ok_seqs(seqs)) return ATTAMBA_ERR_INVALID_ARG;
+  if (too_many(seqs->slots, seqs->S, "attamba_selective_scan")) return ATTAMBA_ERR_UNSUPPORTED;
   attamba::SelScanArgs a{};
   a.x = x; a.dt = dt; a.Bm = B; a.Cm = C; a.z = z; a.bias = bias; a.A = A; a.skip = skip; a.state = state; a.y = y;
   a.cu = seqs->cu; a.slots = seqs->slots; a.cont = seqs->cont;
@@ -485,7 +498,8 @@ attamba_status_t attamba_scan_step(attamba_dtype_t dtype, const void* x, int64_t
                                    int64_t ldc, const float* skip, const void* z, int64_t ldz, int32_t D, int32_t N,
                                    int32_t rows, const int32_t* slots, float* state, int32_t n_slots, void* y,
                                    int64_t ldy, int32_t* d_status, attamba_stream_t stream) {
-  if (rows < 1 || rows > kMaxRows || !state) return ATTAMBA_ERR_INVALID_ARG;
+  if (rows < 1 || !state) return ATTAMBA_ERR_INVALID_ARG;
+  if (too_many(slots, rows, "attamba_scan_step")) return ATTAMBA_ERR_UNSUPPORTED;
   attamba::SelScanArgs a{};
   a.x = x; a.dt = dt; a.Bm = B; a.Cm = C; a.z = z; a.bias = bias; a.A = A; a.skip = skip; a.state = state; a.y = y;
   a.slots = slots;

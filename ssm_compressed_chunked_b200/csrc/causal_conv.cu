@@ -205,15 +205,14 @@ __global__ void __launch_bounds__(32 * kConvWarps) causal_conv_kernel(ConvArgs p
 template <typename T, int K, bool SILU>
 __global__ void __launch_bounds__(32 * kStepWarps) conv_step_kernel(ConvArgs p) {
   using raw = typename Pack<T>::raw;
+  __shared__ SlotTable table;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t b = (int64_t)blockIdx.x * kStepWarps + warp;
-  if (b >= p.T) return;
-  const int slot = p.slots ? p.slots[b] : (int)b;
-  if (slot == -1) return;
+  const int first = blockIdx.x * kStepWarps, b = first + warp;
   // every load goes out before the slot is known to be good: one in range is safe to read
+  const int slot = b < p.T ? (p.slots ? __ldg(p.slots + b) : b) : -1;
   const int c0 = (blockIdx.y * 32 + lane) * kV;
-  const bool active = c0 < p.D;
+  const bool active = c0 < p.D && slot != -1;
   T* st = static_cast<T*>(p.state) + (size_t)(slot >= 0 && slot < p.n_slots ? slot : 0) * (K - 1) * p.D + c0;
   Taps<T, K> taps;
   float2 win[K - 1][2];
@@ -221,11 +220,12 @@ __global__ void __launch_bounds__(32 * kStepWarps) conv_step_kernel(ConvArgs p) 
   if (active) {
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) Pack<T>::unpack(*reinterpret_cast<const raw*>(st + (size_t)k * p.D), win[k]);
-    x = __ldg(reinterpret_cast<const raw*>(static_cast<const T*>(p.x) + b * p.ldx + c0));
+    x = __ldg(reinterpret_cast<const raw*>(static_cast<const T*>(p.x) + (int64_t)b * p.ldx + c0));
     taps.load(p, c0);
   }
-  if (state_slot_warp(p.slots, (int)b, p.n_slots, lane, p.status) < 0 || !active) return;
-  *reinterpret_cast<raw*>(static_cast<T*>(p.y) + b * p.ldy + c0) = taps.template step<SILU>(win, x);
+  const int good = state_slots_block(p.slots, first, 1, min((int)p.T, first + kStepWarps), p.n_slots, table, p.status);
+  if (__shfl_sync(0xffffffffu, good, warp) < 0 || !active) return;
+  *reinterpret_cast<raw*>(static_cast<T*>(p.y) + (int64_t)b * p.ldy + c0) = taps.template step<SILU>(win, x);
 #pragma unroll
   for (int k = 0; k < K - 1; ++k) *reinterpret_cast<raw*>(st + (size_t)k * p.D) = Pack<T>::pack(win[k]);
 }

@@ -171,31 +171,48 @@ __device__ __forceinline__ int state_slot_warp(const int32_t* slots, int s, int 
   return slot;
 }
 
-// state_slot_warp for up to 32 batch rows first, first + stride, ... < rows at once: lane j gets row j's answer.  The
-// slots ahead of the rows are read once for all of them.
-__device__ __forceinline__ int state_slots_warp(const int32_t* slots, int first, int stride, int rows, int n_slots,
-                                                int lane, int32_t* st) {
+// state_slot_warp for up to 32 batch rows first, first + stride, ... < rows at once, by a whole block: lane j of every
+// warp gets row j's answer.  The rows' slots go into a small hash table (a bit per row); each slot ahead of the last row
+// then costs one look-up, however many rows there are.
+struct SlotTable {
+  static constexpr int kEntries = 256;
+  uint32_t rows[kEntries];   // by slot mod kEntries: which rows have such a slot
+  int slot[32];
+  uint32_t repeated;
+};
+__device__ __forceinline__ int state_slots_block(const int32_t* slots, int first, int stride, int rows, int n_slots,
+                                                 SlotTable& t, int32_t* st) {
+  const int lane = threadIdx.x & 31;
   const int64_t mine = first + (int64_t)lane * stride;
   int slot = mine < rows ? (slots ? __ldg(slots + mine) : (int)mine) : -1;
   bool bad = slot != -1 && (slot < 0 || slot >= n_slots);
   if (slots) {
     const int n = min(32, (rows - first + stride - 1) / stride);
     const int last = first + (n - 1) * stride;   // slots[0, last) lie ahead of some row
-    for (int j = lane; j - lane < last; j += 128) {
-      int v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = j + 32 * u < last ? __ldg(slots + j + 32 * u) : -1;
-      for (int i = 0; i < n; ++i) {
-        const int s = __shfl_sync(0xffffffffu, slot, i), b = first + i * stride;
-        bool same = false;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) same |= v[u] == s && j + 32 * u < b;
-        if (__any_sync(0xffffffffu, same) && lane == i && slot != -1) bad = true;
+    __syncthreads();                             // the table's last use is over
+    for (int i = threadIdx.x; i < SlotTable::kEntries; i += blockDim.x) t.rows[i] = 0;
+    if (threadIdx.x == 0) t.repeated = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      t.slot[lane] = slot;
+      if (slot >= 0) atomicOr(&t.rows[slot % SlotTable::kEntries], 1u << lane);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int j = threadIdx.x; j < last; j += blockDim.x) {
+      const int v = __ldg(slots + j);
+      uint32_t m = v >= 0 ? t.rows[v % SlotTable::kEntries] : 0;
+      while (m) {
+        const int i = __ffs(m) - 1;
+        m &= m - 1;
+        if (t.slot[i] == v && j < first + i * stride) atomicOr(&t.repeated, 1u << i);
       }
     }
+    __syncthreads();
+    bad |= slot != -1 && ((t.repeated >> lane) & 1);
   }
   if (bad) {
-    raise_status(st, ATTAMBA_DEV_BAD_SEQS);
+    if (threadIdx.x < 32) raise_status(st, ATTAMBA_DEV_BAD_SEQS);
     slot = -1;
   }
   return slot;

@@ -516,8 +516,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) scan_join_kernel(SelScanArgs 
 // state accesses are 16 bytes a lane, 128 bytes of a state row a quarter.  A block walks several batch rows of its
 // 128 channels: A stays in registers, each thread copies its part of the next row's state into a ring of its own
 // (cp.async, no barrier) and loads the next row's inputs while it computes this one's.  Bound by reading and writing
-// the state: 251 rows x 2048 channels x 16 in 16.4 us (4.2 TB/s; a copy of these rows in the same pattern takes 14.9),
-// 256 x 4096 x 32 in 52 us (5.2 TB/s).  One row a block with everything in registers: 18.1 and 60.
+// the state: 251 rows x 2048 channels x 16 in 16.2 us (4.3 TB/s; a copy of these rows in the same pattern takes 14.9),
+// 256 x 4096 x 32 in 51 us (5.4 TB/s).  One row a block with everything in registers: 18.1 and 60.  The search for
+// repeated slots (a hash table of the block's rows): 4096 x 1024 x 16 in 113 us, 91 without a slot map, 188 with
+// every row compared with every slot ahead of it.
 template <typename T> struct Four;
 template <> struct Four<float> {
   using raw = float4;
@@ -542,6 +544,7 @@ template <typename T, int NS>
 __global__ void __launch_bounds__(kThreads, step_blocks(NS)) scan_step_kernel(SelScanArgs p, int groups) {
   constexpr int NPL = NS / 4;
   __shared__ __align__(16) float4 ring[kStepDepth][NPL][kThreads];
+  __shared__ SlotTable table;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = (((int)blockIdx.x % groups) * (kThreads / 32) + warp) * 32 + (lane & 7) * 4;
@@ -605,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, step_blocks(NS)) scan_step_kernel(Se
   load(first);
   int good = -1;   // lane j: the state row of batch row i + j (i a multiple of 32), while the first states are under way
   for (int i = 0, b = first; b < rows; ++i, b += stride) {
-    if (i % 32 == 0) good = state_slots_warp(p.slots, b, stride, rows, p.n_slots, lane, p.status);
+    if (i % 32 == 0) good = state_slots_block(p.slots, b, stride, rows, p.n_slots, table, p.status);   // i is the block's
     const int here = __shfl_sync(0xffffffffu, good, i % 32);
     float x[4], Bn[NPL], Cn[NPL];
     Four<T>::unpack(rx, x);

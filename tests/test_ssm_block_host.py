@@ -75,6 +75,15 @@ def test_selective_scan_refuses(kw, code):
     assert _scan(**kw) == code
 
 
+def test_more_sequences_than_a_call_takes_are_refused():
+    many, slots = (1 << 20) + 1, FAKE
+    assert _conv(seqs=_seqs(S=many)) == UNS and _scan(seqs=_seqs(S=many)) == UNS
+    assert _conv(seqs=_seqs(S=8193, slots=slots)) == UNS and _scan(seqs=_seqs(S=8193, slots=slots)) == UNS
+    assert b"at most 8192 with slots" in A.load().attamba_last_error()
+    assert _conv_step(B=many) == UNS and _conv_step(B=8193, slots=slots) == UNS
+    assert _scan_step(rows=many) == UNS
+
+
 def test_selective_scan_says_how_much_workspace_it_needs():
     assert _scan(seqs=_seqs(T=4096)) == INV
     assert b"bytes of workspace" in A.load().attamba_last_error()
