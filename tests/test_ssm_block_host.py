@@ -129,3 +129,12 @@ def test_the_binding_refuses_cpu_tensors_and_other_objects():
         A.conv_step(None, w, None, st, x)
     with pytest.raises(A.AttambaError, match="w must be a tensor|CUDA"):
         A.conv_step(x, [1, 2], None, st, x)
+
+
+def test_the_binding_shares_the_process_cxx_runtime():
+    """The marshalling module needs the C++ runtime as a shared library, like torch: a copy of its own linked in would
+    be a second one in the process, whose exceptions and locales are not the first's."""
+    import subprocess
+    from ssm_compressed_chunked_b200 import build
+    out = subprocess.run(["readelf", "-d", build.BINDING], capture_output=True, text=True, check=True).stdout
+    assert "libstdc++.so" in out and "libtorch_python.so" in out
