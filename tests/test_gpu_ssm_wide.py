@@ -1,5 +1,6 @@
-"""Element offsets past 2^31 in the SSM block's operators: token rows 65536 bytes apart and states of more than 2^31
-elements.  The rows past the 32-bit border are compared with the oracle, which sees the same tokens next to each other."""
+"""The SSM block's operators at width: element offsets past 2^31 (token rows 65536 bytes apart, states of more than 2^31
+elements; the rows past the border are compared with the oracle, which sees the same tokens next to each other), the scan's
+variants for long and wide batches on sampled channels, and two streams on one state array."""
 
 import numpy as np
 import pytest
@@ -9,7 +10,7 @@ from block_cases import HALF, TINY, U, assert_within, offsets, scan_bound, scan_
 from helpers import f64
 from oracle import block as OB
 from ssm_compressed_chunked_b200 import attamba as A
-from test_gpu_ssm_block import conv_bound, i32, new_status, workspace
+from test_gpu_ssm_block import conv_bound, i32, new_status, run_scan, workspace
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -114,3 +115,68 @@ def test_states_past_2_31_elements():
     assert status.item() == 0 and float(st[n_slots // 2].abs().max()) == 0.0
     del st
     torch.cuda.empty_cache()
+
+
+def channels_of(d, pick):
+    """The scan's inputs restricted to some channels (they do not mix; B and C are shared)."""
+    cut = lambda k, v: None if v is None else v[:, pick] if k in ("x", "dt", "z") else v[pick] if k in ("A", "bias", "skip") else v  # noqa: E731
+    return {k: cut(k, v) for k, v in d.items()}
+
+
+# one lane a channel from 2^27 tokens x channels x states on, two below, four for narrow blocks; ragged sequences that end inside
+# and on tiles' ends, empty ones, kept and fresh states
+@pytest.mark.parametrize("dtype,D,N,lens,pad", [("bf16", 2048, 16, [1500, 0, 37, 2000, 1, 600], 5), ("f32", 2048, 16, [4100], 0),
+                                                ("bf16", 2048, 32, [700, 1399], 3), ("f32", 1024, 32, [4096], 0),
+                                                ("bf16", 512, 16, [300, 0, 1, 512, 77], 9), ("f32", 512, 32, [130, 500], 0),
+                                                ("bf16", 1024, 16, [2048], 0), ("f32", 2056, 16, [129], 2)])
+def test_scan_variants_on_sampled_channels(dtype, D, N, lens, pad):
+    dt = {"bf16": BF, "f32": torch.float32}[dtype]
+    T, S = sum(lens) + pad, len(lens)
+    d = scan_inputs(T, D, N, dt, seed=D + N + S)
+    cu = offsets(lens)
+    rng = np.random.default_rng(S)
+    slots, cont = rng.permutation(S + 2)[:S], rng.integers(0, 2, S)
+    state = torch.randn(S + 2, N, D, generator=torch.Generator().manual_seed(S))
+    y, st, status = run_scan(d, cu, T, dt, state, slots, cont)
+    assert status == 0
+    pick = sorted({0, 1, 31, 32, 127, 128, 255, 256, D // 2 - 1, D // 2, D - 2, D - 1})
+    part = channels_of(d, pick)
+    n = {k: f64(v) for k, v in part.items()}
+    ref, ref_st = OB.selective_scan(n["x"], n["dt"], n["bias"], n["A"], n["B"], n["C"], cu, n["skip"], n["z"],
+                                    f64(state[:, :, pick]), slots, cont)
+    by, bst = scan_bound(part, cu, dt, state[:, :, pick], slots, cont)
+    m = sum(lens)
+    assert bool(torch.isnan(y[m:]).all()) and not bool(torch.isnan(y[:m]).any())
+    assert_within(f64(y[:m][:, pick]), ref[:m], by[:m], "y")
+    assert_within(f64(st[:, :, pick])[slots], ref_st[slots], bst[slots], "state")
+
+
+def test_two_streams_share_a_state_array():
+    """Prompts and steps of disjoint slots of one state array on two streams at once, a workspace each, against the same
+    calls one after the other."""
+    D, N, T = 512, 16, 500
+    both = [scan_inputs(T, D, N, BF, seed=60 + k) for k in range(2)]
+    g = [{k: v.cuda() for k, v in d.items()} for d in both]
+    start = torch.randn(8, N, D, generator=torch.Generator().manual_seed(7)).cuda()
+    slots = [i32([0, 2, 4, 6]), i32([7, 5, 3, 1])]
+    seqs = [A.Seqs(i32([0, 100, 100, 333, 500]), T, slots=s, cont=i32([1, 0, 1, 1])) for s in slots]
+    ws = [workspace(T, D, N) for _ in range(2)]
+
+    def calls(k, st, out):
+        a = g[k]
+        for _ in range(10):
+            A.selective_scan(a["x"], a["dt"], a["bias"], a["A"], a["B"], a["C"], seqs[k], out, skip=a["skip"], z=a["z"],
+                             state=st, workspace=ws[k])
+            A.scan_step(a["x"][:4], a["dt"][:4], a["bias"], a["A"], a["B"][:4], a["C"][:4], st, out[:4], slots=slots[k])
+
+    st1, out1 = start.clone(), [torch.zeros(T, D, dtype=BF, device="cuda") for _ in range(2)]
+    for k in range(2):
+        calls(k, st1, out1[k])
+    st2, out2 = start.clone(), [torch.zeros(T, D, dtype=BF, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for k in range(2):
+        with torch.cuda.stream(streams[k]):
+            calls(k, st2, out2[k])
+    torch.cuda.synchronize()
+    assert torch.equal(st1, st2) and all(torch.equal(a, b) for a, b in zip(out1, out2))
