@@ -217,7 +217,8 @@ class SsmMixer:
 
     ``weights``: W_in [2 Di, D], W_x [Di + 2 N, Di] (rows dt, B, C), W_O [D, Di] bf16 in [out, in] layout; conv_w
     [Di, K], A [Di, N] f32; conv_b, bias (of the step), skip [Di] f32 or absent.  D and Di are multiples of 64.
-    ``max_tokens`` bounds a call's token rows; the buffers are made once."""
+    ``max_tokens`` bounds a call's token rows; the buffers are made once.  Rows of no sequence (behind the last
+    prompt, or with slot -1 in a step) come back with nothing of use in them."""
 
     def __init__(self, D, Di, N, K, weights, max_tokens, device="cuda", alloc=None):
         bf, f32 = torch.bfloat16, torch.float32

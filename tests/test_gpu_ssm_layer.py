@@ -189,3 +189,40 @@ def test_mixer_refuses_wrong_weights_and_too_many_tokens():
     with pytest.raises(A.AttambaError, match="holds 1 to 8"):
         mix.forward(h, A.Seqs(i32([0, 9]), 9))
     assert mix.forward(h[:8], A.Seqs(i32([0, 8]), 8)).abs().max().item() == 0.0
+
+
+def test_decode_step_in_a_captured_graph():
+    """Two blocks' decode step captured once and replayed, new tokens copied into its input, against eager steps: the same
+    streams and states, bit for bit."""
+    D, Di, N, K, B = 128, 256, 16, 4, 5
+    mixers = [layer.SsmMixer(D, Di, N, K, cuda(mixer_weights(D, Di, N, K, 20 + k)), B) for k in range(2)]
+    g = torch.Generator().manual_seed(2)
+    norms = [torch.rand(D, generator=g).cuda() + 0.5 for _ in range(4)]
+    blocks = [layer.Block(m, norms[k], w_post=norms[2 + k], alpha=0.7) for k, m in enumerate(mixers)]
+    slots = i32([3, 0, -1, 5, 1])
+    tokens = torch.randn(4, B, D, generator=g).cuda()
+
+    def step(states, r):
+        h = None
+        for k, b in enumerate(blocks):
+            r, h = b.decode_step(states[k], r, h=h, slots=slots, next_norm=norms[1] if k == 0 else None)
+        return r
+
+    eager_states = [m.new_state(6) for m in mixers]
+    eager = [step(eager_states, t.clone()).clone() for t in tokens]
+    states, r = [m.new_state(6) for m in mixers], tokens[0].clone()
+    step(states, r)                      # warm-up ahead of the capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(states, r)
+    for win, ssm in states:
+        win.zero_()
+        ssm.zero_()
+    live = [0, 1, 3, 4]                  # row 2 fills the batch up: its mixer output is what the buffer held
+    for t, want in zip(tokens, eager):
+        r.copy_(t)
+        graph.replay()
+        assert torch.equal(r[live], want[live])
+    for (win, ssm), (ewin, essm) in zip(states, eager_states):
+        assert torch.equal(win, ewin) and torch.equal(ssm, essm)
+    assert all(m.status.item() == 0 for m in mixers)
