@@ -101,7 +101,8 @@ typedef struct {
 const char* attamba_version(void);
 /* Static text of a status code. */
 const char* attamba_status_string(attamba_status_t s);
-/* CUDA error text of this thread's last ATTAMBA_ERR_CUDA ("" if none). */
+/* CUDA error text of this thread's last ATTAMBA_ERR_CUDA ("" if none), or the reason of the last refusal that
+ * gives one (the SSM block's operators give one for every refusal). */
 const char* attamba_last_error(void);
 
 /* Chunks per sequence for uniform chunking of size P with cyclic offset

@@ -337,6 +337,13 @@ attamba_status_t attamba_decode_step_noalloc(attamba_dtype_t dtype, const attamb
 }
 
 namespace {
+// A refusal with its reason as the thread's error text.
+attamba_status_t refuse(attamba_status_t st, const char* what, const char* why) {
+  snprintf(g_err, sizeof(g_err), "%s: %s", what, why);
+  return st;
+}
+constexpr attamba_status_t kInvalid = ATTAMBA_ERR_INVALID_ARG, kUnsupported = ATTAMBA_ERR_UNSUPPORTED;
+
 // Token rows an operator of the SSM block reads or writes: rows x cols elements of `es` bytes, `ld` apart.
 struct Rows {
   const void* p;
@@ -397,11 +404,14 @@ bool ok_seqs(const attamba_seqs_t* q) {
 
 attamba_status_t conv_entry(attamba_dtype_t dtype, attamba::ConvArgs& a, int64_t ldx, int64_t ldy, int32_t K,
                             attamba_act_t act, bool step, cudaStream_t s, const char* name) {
-  if (!ok_dtype(dtype) || K < 2 || K > 4) return ATTAMBA_ERR_UNSUPPORTED;
-  if (!a.x || !a.w || !a.y || !ok_channels(a.D) || (act != ATTAMBA_ACT_LINEAR && act != ATTAMBA_ACT_SILU))
-    return ATTAMBA_ERR_INVALID_ARG;
-  if ((a.state && a.n_slots < 1) || !aligned16(a.w) || !aligned16(a.bias) || !aligned16(a.state))
-    return ATTAMBA_ERR_INVALID_ARG;
+  if (!ok_dtype(dtype)) return refuse(kUnsupported, name, "dtype is F32 or BF16");
+  if (K < 2 || K > 4) return refuse(kUnsupported, name, "K is 2, 3 or 4");
+  if (!a.x || !a.w || !a.y) return refuse(kInvalid, name, "x, w and y are required");
+  if (!ok_channels(a.D)) return refuse(kInvalid, name, "D is a multiple of 8, at most 2^20");
+  if (act != ATTAMBA_ACT_LINEAR && act != ATTAMBA_ACT_SILU) return refuse(kInvalid, name, "act is LINEAR or SILU");
+  if (a.state && a.n_slots < 1) return refuse(kInvalid, name, "a state has at least one slot");
+  if (!aligned16(a.w) || !aligned16(a.bias) || !aligned16(a.state))
+    return refuse(kInvalid, name, "w, bias and state are 16-byte aligned");
   const int es = elem_size(dtype);
   const Rows rows[] = {{a.x, a.T, ldx, a.D, es, false, "x"},
                        {a.y, a.T, ldy, a.D, es, true, "y"},
@@ -417,10 +427,13 @@ attamba_status_t conv_entry(attamba_dtype_t dtype, attamba::ConvArgs& a, int64_t
 
 attamba_status_t check_scan(attamba_dtype_t dtype, attamba::SelScanArgs& a, int64_t ldx, int64_t lddt, int64_t ldb,
                             int64_t ldc, int64_t ldz, int64_t ldy, const char* name) {
-  if (!ok_dtype(dtype) || (a.N != 16 && a.N != 32)) return ATTAMBA_ERR_UNSUPPORTED;
-  if (!a.x || !a.dt || !a.A || !a.Bm || !a.Cm || !a.y || !ok_channels(a.D)) return ATTAMBA_ERR_INVALID_ARG;
-  if (!aligned16(a.A) || !aligned16(a.bias) || !aligned16(a.skip) || (a.state && a.n_slots < 1))
-    return ATTAMBA_ERR_INVALID_ARG;
+  if (!ok_dtype(dtype)) return refuse(kUnsupported, name, "dtype is F32 or BF16");
+  if (a.N != 16 && a.N != 32) return refuse(kUnsupported, name, "N is 16 or 32");
+  if (!a.x || !a.dt || !a.A || !a.Bm || !a.Cm || !a.y) return refuse(kInvalid, name, "x, dt, A, B, C and y are required");
+  if (!ok_channels(a.D)) return refuse(kInvalid, name, "D is a multiple of 8, at most 2^20");
+  if (a.state && a.n_slots < 1) return refuse(kInvalid, name, "a state has at least one slot");
+  if (!aligned16(a.A) || !aligned16(a.bias) || !aligned16(a.skip))
+    return refuse(kInvalid, name, "A, bias and skip are 16-byte aligned");
   const int es = elem_size(dtype);
   const Rows rows[] = {{a.x, a.T, ldx, a.D, es, false, "x"},   {a.dt, a.T, lddt, a.D, es, false, "dt"},
                        {a.Bm, a.T, ldb, a.N, es, false, "B"},  {a.Cm, a.T, ldc, a.N, es, false, "C"},
@@ -442,7 +455,7 @@ attamba_status_t attamba_causal_conv(attamba_dtype_t dtype, const void* x, int64
                                      const float* bias, int32_t D, int32_t K, attamba_act_t act,
                                      const attamba_seqs_t* seqs, void* state, int32_t n_slots, void* y,
                                      int64_t ldy, int32_t* d_status, attamba_stream_t stream) {
-  if (!ok_seqs(seqs)) return ATTAMBA_ERR_INVALID_ARG;
+  if (!ok_seqs(seqs)) return refuse(kInvalid, "attamba_causal_conv", "a sequence table has cu, S >= 1 and 1 <= T < 2^31 - 65536");
   if (too_many(seqs->slots, seqs->S, "attamba_causal_conv")) return ATTAMBA_ERR_UNSUPPORTED;
   attamba::ConvArgs a{};
   a.x = x; a.w = w; a.bias = bias; a.state = state; a.y = y;
@@ -455,7 +468,7 @@ attamba_status_t attamba_conv_step(attamba_dtype_t dtype, const void* x, int64_t
                                    const float* bias, int32_t D, int32_t K, attamba_act_t act, int32_t B,
                                    const int32_t* slots, void* state, int32_t n_slots, void* y, int64_t ldy,
                                    int32_t* d_status, attamba_stream_t stream) {
-  if (B < 1 || !state) return ATTAMBA_ERR_INVALID_ARG;
+  if (B < 1 || !state) return refuse(kInvalid, "attamba_conv_step", "B >= 1 and a state are required");
   if (too_many(slots, B, "attamba_conv_step")) return ATTAMBA_ERR_UNSUPPORTED;
   attamba::ConvArgs a{};
   a.x = x; a.w = w; a.bias = bias; a.state = state; a.y = y; a.slots = slots;
@@ -474,7 +487,7 @@ attamba_status_t attamba_selective_scan(attamba_dtype_t dtype, const void* x, in
                                         int64_t ldz, int32_t D, int32_t N, const attamba_seqs_t* seqs, float* state,
                                         int32_t n_slots, void* y, int64_t ldy, void* workspace,
                                         size_t workspace_bytes, int32_t* d_status, attamba_stream_t stream) {
-  if (!ok_seqs(seqs)) return ATTAMBA_ERR_INVALID_ARG;
+  if (!ok_seqs(seqs)) return refuse(kInvalid, "attamba_selective_scan", "a sequence table has cu, S >= 1 and 1 <= T < 2^31 - 65536");
   if (too_many(seqs->slots, seqs->S, "attamba_selective_scan")) return ATTAMBA_ERR_UNSUPPORTED;
   attamba::SelScanArgs a{};
   a.x = x; a.dt = dt; a.Bm = B; a.Cm = C; a.z = z; a.bias = bias; a.A = A; a.skip = skip; a.state = state; a.y = y;
@@ -498,7 +511,7 @@ attamba_status_t attamba_scan_step(attamba_dtype_t dtype, const void* x, int64_t
                                    int64_t ldc, const float* skip, const void* z, int64_t ldz, int32_t D, int32_t N,
                                    int32_t rows, const int32_t* slots, float* state, int32_t n_slots, void* y,
                                    int64_t ldy, int32_t* d_status, attamba_stream_t stream) {
-  if (rows < 1 || !state) return ATTAMBA_ERR_INVALID_ARG;
+  if (rows < 1 || !state) return refuse(kInvalid, "attamba_scan_step", "rows >= 1 and a state are required");
   if (too_many(slots, rows, "attamba_scan_step")) return ATTAMBA_ERR_UNSUPPORTED;
   attamba::SelScanArgs a{};
   a.x = x; a.dt = dt; a.Bm = B; a.Cm = C; a.z = z; a.bias = bias; a.A = A; a.skip = skip; a.state = state; a.y = y;
@@ -515,14 +528,18 @@ attamba_status_t attamba_block_norm(attamba_dtype_t dtype, attamba_dtype_t res_d
                                     const float* w_post, const void* res, int64_t ldr, const float* scale,
                                     float alpha, const float* w_pre, float eps, int64_t M, int32_t D, void* res_out,
                                     int64_t ldro, void* h, int64_t ldh, attamba_stream_t stream) {
-  if (!ok_dtype(dtype) || !ok_dtype(res_dtype)) return ATTAMBA_ERR_UNSUPPORTED;
-  if (D < 8 || D % 8 != 0 || M < 1 || M > 0x7fffffff) return ATTAMBA_ERR_INVALID_ARG;
-  if (D > attamba::kMaxNormDim) return ATTAMBA_ERR_UNSUPPORTED;
-  if (!(eps >= 0.f) || (!y && !res) || (!res_out && !h) || (h == nullptr) != (w_pre == nullptr))
-    return ATTAMBA_ERR_INVALID_ARG;
-  if (!y && (gate || w_post || scale)) return ATTAMBA_ERR_INVALID_ARG;
-  if (act != ATTAMBA_ACT_LINEAR && act != ATTAMBA_ACT_SILU && act != ATTAMBA_ACT_SIGMOID) return ATTAMBA_ERR_INVALID_ARG;
-  if (!aligned16(w_post) || !aligned16(scale) || !aligned16(w_pre)) return ATTAMBA_ERR_INVALID_ARG;
+  const char* name = "attamba_block_norm";
+  if (!ok_dtype(dtype) || !ok_dtype(res_dtype)) return refuse(kUnsupported, name, "dtype and res_dtype are F32 or BF16");
+  if (D < 8 || D % 8 != 0 || M < 1 || M > 0x7fffffff) return refuse(kInvalid, name, "D is a multiple of 8, 1 <= M < 2^31");
+  if (D > attamba::kMaxNormDim) return refuse(kUnsupported, name, "D is at most 32768");
+  if (!(eps >= 0.f)) return refuse(kInvalid, name, "eps >= 0");
+  if ((!y && !res) || (!res_out && !h)) return refuse(kInvalid, name, "y or res, and res_out or h, are required");
+  if ((h == nullptr) != (w_pre == nullptr)) return refuse(kInvalid, name, "h and w_pre go together");
+  if (!y && (gate || w_post || scale)) return refuse(kInvalid, name, "gate, w_post and scale belong to y");
+  if (act != ATTAMBA_ACT_LINEAR && act != ATTAMBA_ACT_SILU && act != ATTAMBA_ACT_SIGMOID)
+    return refuse(kInvalid, name, "act is LINEAR, SILU or SIGMOID");
+  if (!aligned16(w_post) || !aligned16(scale) || !aligned16(w_pre))
+    return refuse(kInvalid, name, "w_post, scale and w_pre are 16-byte aligned");
   const int es = elem_size(dtype), rs = elem_size(res_dtype);
   // an output in place of its input is written by the thread that read it, after the row's last read
   const bool in_place_r = res_out && res_out == res && ldro == ldr, in_place_h = h && h == y && ldh == ldy;
@@ -531,14 +548,14 @@ attamba_status_t attamba_block_norm(attamba_dtype_t dtype, attamba_dtype_t res_d
                        {in_place_r ? nullptr : res, M, ldr, D, rs, false, "res"},
                        {res_out, M, ldro, D, rs, true, "res_out"},
                        {h, M, ldh, D, es, true, "h"}};
-  const attamba_status_t st = check_rows(rows, 5, "attamba_block_norm");
+  const attamba_status_t st = check_rows(rows, 5, name);
   if (st != ATTAMBA_OK) return st;
   attamba::NormArgs a{};
   a.y = y; a.gate = gate; a.res = res; a.w_post = w_post; a.scale = scale; a.w_pre = w_pre; a.res_out = res_out; a.h = h;
   a.ldy = ldy; a.ldg = ldg; a.ldr = ldr; a.ldro = ldro; a.ldh = ldh;
   a.M = M; a.D = D; a.act = (int32_t)act; a.gate_first = gate_first; a.alpha = alpha; a.eps = eps;
   const cudaError_t e = attamba::launch_block_norm(dtype, res_dtype, a, reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? ATTAMBA_OK : cuda_fail(e, "attamba_block_norm");
+  return e == cudaSuccess ? ATTAMBA_OK : cuda_fail(e, name);
 }
 
 }  // extern "C"

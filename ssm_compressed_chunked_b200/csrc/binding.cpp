@@ -181,8 +181,8 @@ bool stream_of(PyObject* o, int dev, const char* what, attamba_stream_t& out) {
 bool check(attamba_status_t st, const char* what) {
   if (st == ATTAMBA_OK) return true;
   std::string text = std::string(what) + ": " + g_status_string(st);
-  const char* more = g_last_error();
-  if (more && *more) text += std::string(" ") + more;
+  const char* more = g_last_error();   // every refusal of these entry points says why
+  if (more && *more) text += std::string(" (") + more + ")";
   return refuse(text);
 }
 

@@ -75,6 +75,18 @@ def test_selective_scan_refuses(kw, code):
     assert _scan(**kw) == code
 
 
+def test_every_refusal_says_why():
+    """The thread's error text is the reason of the refusal at hand, not one left from before."""
+    err = lambda: A.load().attamba_last_error().decode()  # noqa: E731
+    for call, kw, why in ((_conv, dict(K=5), "K is"), (_conv, dict(y=FAKE), "y overlaps x"), (_conv, dict(D=60), "D is"),
+                          (_conv, dict(seqs=_seqs(T=0)), "sequence table"), (_conv_step, dict(state=None), "a state"),
+                          (_scan, dict(N=24), "N is"), (_scan, dict(dt=None), "required"), (_scan, dict(Aw=FAKE + 4), "aligned"),
+                          (_scan, dict(ldb=12), "row stride"), (_scan_step, dict(n=0), "slot"), (_norm, dict(eps=-1.0), "eps"),
+                          (_norm, dict(h=None), "go together"), (_norm, dict(D=32776), "32768"), (_norm, dict(act=3), "act is")):
+        assert call(**kw) in (INV, UNS)
+        assert why in err() and err().startswith("attamba_"), (kw, err())
+
+
 def test_more_sequences_than_a_call_takes_are_refused():
     many, slots = (1 << 20) + 1, FAKE
     assert _conv(seqs=_seqs(S=many)) == UNS and _scan(seqs=_seqs(S=many)) == UNS
