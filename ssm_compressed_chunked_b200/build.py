@@ -42,9 +42,10 @@ def _gxx(out):
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), sysconfig.get_paths()["include"], INCLUDE]
-    # nvcc's host compiler, whatever CXX says: the module shares torch's C++ runtime, and a compiler that links one
+    # the system's compiler, whatever CXX says: the module shares torch's C++ runtime, and a compiler that links one
     # of its own into it would leave two in the process
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    cxx = "/usr/bin/g++" if os.path.exists("/usr/bin/g++") else "g++"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [f"-I{d}" for d in inc] + \
         [os.path.join(CSRC, "binding.cpp"), "-o", out + ".tmp", "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda",
          "-ltorch_cpu", "-ltorch_python"]
