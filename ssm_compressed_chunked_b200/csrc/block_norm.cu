@@ -85,8 +85,19 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kWarpRows : TPR) block_norm_k
   const int D = p.D;
   // A thread with one vector loads all of its row first: the two sums would otherwise each put a memory latency ahead of the next
   // load (16384 x 2048, fp32 residual: 70.8 against 76.2 us).  With more vectors the registers that takes cost more
-  // blocks than it gives (4096 x 8192: 65 against 56 us), and gate and residual are loaded where they are used.
-  constexpr bool kFirst = VPT == 1;
+  // blocks than it gives (4096 x 8192: 65 against 56 us): there gate and residual are loaded where they are used, but
+  // a bf16 residual waits in shared memory (8192 x 4096: 47.2 against 51.0 us, 4096 x 8192 52.8 against 56.3); an fp32
+  // one takes twice the room and lost as much (4096 x 6000: 82.6 against 75.8).
+  constexpr bool kFirst = VPT == 1, kAsync = VPT > 1 && sizeof(R) == 2 && TPR * VPT * 16 <= 32768;
+  __shared__ __align__(16) typename Eight<R>::raw ahead[kAsync ? VPT : 1][kAsync ? TPR : 1];   // a thread's own pieces
+  if (kAsync && p.res) {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (id + k * TPR) * 8;
+      if (c < D) copy_async<16>(&ahead[kAsync ? k : 0][kAsync ? id : 0], static_cast<const R*>(p.res) + row * p.ldr + c);
+    }
+    copies_commit();
+  }
   float v[VPT][8];
   typename Eight<T>::raw g[VPT];
   typename Eight<R>::raw r[VPT];
@@ -96,7 +107,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kWarpRows : TPR) block_norm_k
   };
   auto load_res = [&](int k, int c) {
     r[k] = {};
-    if (p.res && c < D) r[k] = Eight<R>::get(static_cast<const R*>(p.res) + row * p.ldr + c);
+    if (p.res && c < D)
+      r[k] = kAsync ? ahead[kAsync ? k : 0][kAsync ? id : 0] : Eight<R>::get(static_cast<const R*>(p.res) + row * p.ldr + c);
   };
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
@@ -140,6 +152,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 32 * kWarpRows : TPR) block_norm_k
   if (p.gate && p.gate_first) gate();
   if (p.w_post) norm(p.w_post);
   if (p.gate && !p.gate_first) gate();
+  if (kAsync) copies_wait<0>();
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int c = (id + k * TPR) * 8;
@@ -175,7 +188,7 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
 template <typename T, typename R>
 cudaError_t launch_for(const NormArgs& a, cudaStream_t s) {
   // threads a row and vectors a thread, measured (B200, GB/s of the copy's 6470): rows of 256 6050, 512 5510, 1024 6180,
-  // 2048 5550 (6640 with an fp32 residual), 4096 5270, 8192 4770, 16384 4080, 32768 3500; from 16384 on an SM holds too
+  // 2048 5660 (6640 with an fp32 residual), 4096 5680, 8192 5080, 16384 4330, 32768 3650; from 16384 on an SM holds too
   // few rows to overlap one's sums with another's loads
   const int vecs = a.D / 8;
   if (vecs <= 32) return launch<T, R, 32, 1>(a, s);
