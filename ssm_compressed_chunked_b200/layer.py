@@ -290,14 +290,31 @@ class Block:
     ``w_pre`` [D] f32 is the norm ahead of the mixer, ``w_post`` (or None) the norm behind it, ``scale`` (or None)
     a per-channel residual scale beside the number ``alpha``.  The residual stream r (bf16 or f32) is updated in
     place.  The pass that adds y to r also makes the next block's input: hand its ``w_pre`` over as ``next_norm``
-    and give the returned h to the next block, whose own first norm then falls away."""
+    and give the returned h to the next block, whose own first norm then falls away.
+
+    ``h`` is what the mixer read in the block's last ``forward`` (handed in or made here): around a Layer it is the
+    x of ``Layer.cache_from_prefill``.  A block that makes its input itself keeps the buffers of it, one for
+    ``forward`` and one for ``decode_step``: like the mixer's own, they serve one call after the other, so calls
+    of a block on several streams are ordered by events."""
 
     def __init__(self, mixer, w_pre, w_post=None, scale=None, alpha=1.0, eps=1e-5):
         self.mixer, self.w_pre, self.w_post, self.scale, self.alpha, self.eps = mixer, w_pre, w_post, scale, alpha, eps
+        self.h = None
+        self._prompt, self._step = [], []   # input buffers, the last one the largest
 
-    def _input(self, r, h, stream):
+    def _buffer(self, kept, r, first, stream):
+        """r.shape rows of bf16 that stay the block's.  Made on the stream that uses them, so that no other stream's
+        pending work holds the memory; freed with the block alone, as a captured graph may hold an address."""
+        n = r.shape[0]
+        if not kept or kept[-1].shape[0] < n:
+            n = max(n, first if not kept else min(2 * kept[-1].shape[0], getattr(self.mixer, "max_tokens", n)))
+            with torch.cuda.stream(stream):
+                kept.append(torch.empty(n, r.shape[1], dtype=torch.bfloat16, device=r.device))
+        return kept[-1][:r.shape[0]]
+
+    def _input(self, r, h, kept, first, stream):
         if h is None:
-            h = torch.empty(r.shape, dtype=torch.bfloat16, device=r.device)
+            h = self._buffer(kept, r, first, stream)
             A.block_norm(None, r, h=h, w_pre=self.w_pre, eps=self.eps, stream=stream)
         return h
 
@@ -309,10 +326,11 @@ class Block:
 
     def forward(self, r, *args, h=None, next_norm=None, stream=None, **kw):
         """r [T, D] -> (r updated, the next block's h or None); the other arguments are the mixer's ``forward``'s."""
-        y = self.mixer.forward(self._input(r, h, stream), *args, stream=stream, **kw)
+        self.h = self._input(r, h, self._prompt, getattr(self.mixer, "max_tokens", 0), stream)
+        y = self.mixer.forward(self.h, *args, stream=stream, **kw)
         return self._join(y, r, next_norm, stream)
 
     def decode_step(self, cache, r, *args, h=None, next_norm=None, stream=None, **kw):
         """The same for one new token per sequence, through the mixer's ``decode_step``."""
-        y = self.mixer.decode_step(cache, self._input(r, h, stream), *args, stream=stream, **kw)
+        y = self.mixer.decode_step(cache, self._input(r, h, self._step, 0, stream), *args, stream=stream, **kw)
         return self._join(y, r, next_norm, stream)
