@@ -380,6 +380,12 @@ attamba_status_t attamba_scan_step(attamba_dtype_t dtype, const void* x, int64_t
                                    int32_t rows, const int32_t* slots, float* state, int32_t n_slots, void* y,
                                    int64_t ldy, int32_t* d_status, attamba_stream_t stream);
 
+/* attamba_clear_rows -- zeros in the rows of y that no sequence owns, which the operators above leave as they are: those
+ * behind a prompt batch's last sequence (seqs given, y [seqs->T, D]), or those of a step with a negative slot (slots
+ * given, y [B, D], B <= 2^20).  One of seqs and slots is NULL.  D and ldy as above. */
+attamba_status_t attamba_clear_rows(attamba_dtype_t dtype, void* y, int64_t ldy, int32_t D, const attamba_seqs_t* seqs,
+                                    int32_t B, const int32_t* slots, attamba_stream_t stream);
+
 /* attamba_block_norm -- the norms after a block and before the next, with gate, residual scale and sum.
  * Per row, with norm(v, w) = v rsqrt(mean(v^2) + eps) w:
  *     v = y;  gate_first: v = v act(gate);  w_post: v = norm(v, w_post);  not gate_first: v = v act(gate)

@@ -33,7 +33,7 @@ EXPORTS = ("attamba_version", "attamba_status_string", "attamba_last_error",
            "attamba_decode_step_noalloc", "attamba_cache_from_prefill",
            "attamba_kv_ssm_scan_u", "attamba_proj_gemm", "attamba_causal_conv", "attamba_conv_step",
            "attamba_selective_scan_workspace_size", "attamba_selective_scan", "attamba_scan_step",
-           "attamba_block_norm")
+           "attamba_clear_rows", "attamba_block_norm")
 
 
 class AttambaError(RuntimeError):
@@ -118,6 +118,8 @@ def load():
     L.attamba_selective_scan.argtypes = scan_args + [ctypes.POINTER(SeqsT), vp, i32, vp, i64, vp, sz, vp, vp]
     L.attamba_scan_step.restype = ctypes.c_int
     L.attamba_scan_step.argtypes = scan_args + [i32, vp, vp, i32, vp, i64, vp, vp]
+    L.attamba_clear_rows.restype = ctypes.c_int
+    L.attamba_clear_rows.argtypes = [ctypes.c_int, vp, i64, i32, ctypes.POINTER(SeqsT), i32, vp, vp]
     L.attamba_block_norm.restype = ctypes.c_int
     L.attamba_block_norm.argtypes = [ctypes.c_int, ctypes.c_int, vp, i64, vp, i64, ctypes.c_int, i32, vp, vp, i64, vp,
                                      f32, vp, f32, i64, i32, vp, i64, vp, i64, vp]
@@ -364,7 +366,7 @@ def _native():
                                "ssm_compressed_chunked_b200.build") from e
         address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
         _binding.init(AttambaError, *(address(getattr(L, "attamba_" + k)) for k in (
-            "status_string", "last_error", "causal_conv", "conv_step", "selective_scan", "scan_step", "block_norm")))
+            "status_string", "last_error", "causal_conv", "conv_step", "selective_scan", "scan_step", "clear_rows", "block_norm")))
         _native_module = _binding
     return _native_module
 
@@ -417,6 +419,13 @@ def selective_scan(x, dt, bias, A, B, C, seqs, y, skip=None, z=None, state=None,
 def scan_step(x, dt, bias, A, B, C, state, y, skip=None, z=None, slots=None, status=None, stream=None):
     """attamba_scan_step: selective_scan for one new token of each row of x [B, D]; ``slots`` as in conv_step."""
     _native().scan_step(x, dt, bias, A, B, C, y, skip, z, state, slots, status, stream)
+
+
+def clear_rows(y, seqs=None, slots=None, stream=None):
+    """attamba_clear_rows: zeros in the rows of y [rows, D] that no sequence owns: behind the last one of ``seqs``, or with a
+    negative slot in ``slots`` [rows] int32 (one of the two)."""
+    at, T, dev = (None, 0, 0) if seqs is None else (seqs.address, seqs.T, seqs.dev)
+    _native().clear_rows(y, at, T, dev, slots, stream)
 
 
 def block_norm(y, res, res_out=None, h=None, w_post=None, w_pre=None, gate=None, gate_act=ACT_SILU, gate_first=False,

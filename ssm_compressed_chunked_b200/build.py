@@ -24,7 +24,7 @@ LIB = os.path.join(HERE, "libattamba.so")
 LIB_CHECKED = os.path.join(HERE, "libattamba_checked.so")
 BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["abi.cu", "chunk_index.cu", "kv_ssm_scan.cu", "chunk_attn.cu", "decode.cu", "handoff.cu", "proj_gemm.cu", "causal_conv.cu",
-           "selective_scan.cu", "block_norm.cu", "device.cu"]
+           "selective_scan.cu", "clear_rows.cu", "block_norm.cu", "device.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-shared", "-cudart", "static", "-I", INCLUDE, "-I", CSRC]

@@ -523,6 +523,25 @@ attamba_status_t attamba_scan_step(attamba_dtype_t dtype, const void* x, int64_t
   return e == cudaSuccess ? ATTAMBA_OK : cuda_fail(e, "attamba_scan_step");
 }
 
+attamba_status_t attamba_clear_rows(attamba_dtype_t dtype, void* y, int64_t ldy, int32_t D, const attamba_seqs_t* seqs,
+                                    int32_t B, const int32_t* slots, attamba_stream_t stream) {
+  const char* name = "attamba_clear_rows";
+  if (!ok_dtype(dtype)) return refuse(kUnsupported, name, "dtype is F32 or BF16");
+  if (!y) return refuse(kInvalid, name, "y is required");
+  if (!ok_channels(D)) return refuse(kInvalid, name, "D is a multiple of 8, at most 2^20");
+  if ((seqs != nullptr) == (slots != nullptr)) return refuse(kInvalid, name, "a sequence table or slots, one of the two");
+  if (seqs && !ok_seqs(seqs)) return refuse(kInvalid, name, "a sequence table has cu, S >= 1 and 1 <= T < 2^31 - 65536");
+  if (seqs ? too_many(nullptr, seqs->S, name) : too_many(nullptr, B, name)) return ATTAMBA_ERR_UNSUPPORTED;
+  if (!seqs && B < 1) return refuse(kInvalid, name, "B >= 1");
+  const int es = elem_size(dtype);
+  const Rows rows[] = {{y, seqs ? seqs->T : B, ldy, D, es, true, "y"}};
+  const attamba_status_t st = check_rows(rows, 1, name);
+  if (st != ATTAMBA_OK) return st;
+  const cudaError_t e = attamba::launch_clear_rows(y, ldy * es, D * es, rows[0].rows, seqs ? seqs->cu + seqs->S : nullptr,
+                                                   slots, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTAMBA_OK : cuda_fail(e, name);
+}
+
 attamba_status_t attamba_block_norm(attamba_dtype_t dtype, attamba_dtype_t res_dtype, const void* y, int64_t ldy,
                                     const void* gate, int64_t ldg, attamba_act_t act, int32_t gate_first,
                                     const float* w_post, const void* res, int64_t ldr, const float* scale,

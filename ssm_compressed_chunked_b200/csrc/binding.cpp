@@ -25,6 +25,7 @@ decltype(&attamba_causal_conv) g_causal_conv = nullptr;
 decltype(&attamba_conv_step) g_conv_step = nullptr;
 decltype(&attamba_selective_scan) g_selective_scan = nullptr;
 decltype(&attamba_scan_step) g_scan_step = nullptr;
+decltype(&attamba_clear_rows) g_clear_rows = nullptr;
 decltype(&attamba_block_norm) g_block_norm = nullptr;
 
 // Every check returns false with the Python error set; what torch itself throws is caught at the entry (entry<>).
@@ -324,6 +325,22 @@ PyObject* scan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              "attamba_scan_step"));
 }
 
+// y, (table address or None, T, device), slots, stream
+PyObject* clear_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Lead l;
+  Rows y;
+  const attamba_seqs_t* q = nullptr;
+  int32_t* slots = nullptr;
+  attamba_stream_t s;
+  if (!count_is(n, 6) || !lead(a[0], "y", l) || !rows(a[0], "y", l.dt, l.rows, l.cols, l.dev, y) ||
+      (a[1] != Py_None && !table(a[1], a[2], a[3], l, q)) || !vec_i32(a[4], "slots", l.rows, l.dev, slots) ||
+      !stream_of(a[5], l.dev, "attamba_clear_rows", s))
+    return nullptr;
+  const OnDevice on(l.dev);
+  return done(on.ok && check(g_clear_rows(l.code, y.p, y.ld, (int32_t)l.cols, q, q ? 0 : (int32_t)l.rows, slots, s),
+                             "attamba_clear_rows"));
+}
+
 // y, res, res_out, h, w_post, w_pre, gate, act, gate_first, scale, alpha, eps, stream
 PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count_is(n, 13)) return nullptr;
@@ -367,14 +384,14 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (AttambaError, addresses of attamba_status_string, _last_error, _causal_conv, _conv_step, _selective_scan, _scan_step,
-// _block_norm)
+// _clear_rows, _block_norm)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 8) {
-    PyErr_SetString(PyExc_TypeError, "init takes the error class and seven addresses");
+  if (n != 9) {
+    PyErr_SetString(PyExc_TypeError, "init takes the error class and eight addresses");
     return nullptr;
   }
-  void* f[7];
-  for (int i = 0; i < 7; ++i) {
+  void* f[8];
+  for (int i = 0; i < 8; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i + 1]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -386,7 +403,8 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_conv_step = reinterpret_cast<decltype(g_conv_step)>(f[3]);
   g_selective_scan = reinterpret_cast<decltype(g_selective_scan)>(f[4]);
   g_scan_step = reinterpret_cast<decltype(g_scan_step)>(f[5]);
-  g_block_norm = reinterpret_cast<decltype(g_block_norm)>(f[6]);
+  g_clear_rows = reinterpret_cast<decltype(g_clear_rows)>(f[6]);
+  g_block_norm = reinterpret_cast<decltype(g_block_norm)>(f[7]);
   Py_RETURN_NONE;
 }
 
@@ -402,7 +420,7 @@ template <Fast F> PyObject* entry(PyObject* self, PyObject* const* a, Py_ssize_t
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(entry<name>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(init),      FAST(causal_conv), FAST(conv_step), FAST(selective_scan),
-                           FAST(scan_step), FAST(block_norm),  {nullptr, nullptr, 0, nullptr}};
+                           FAST(scan_step), FAST(clear_rows),  FAST(block_norm),     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 }  // namespace
 

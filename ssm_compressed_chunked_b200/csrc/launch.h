@@ -167,6 +167,10 @@ size_t selective_scan_workspace_bytes(int64_t T, int32_t D, int32_t N);
 cudaError_t launch_selective_scan(attamba_dtype_t dtype, const SelScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_step(attamba_dtype_t dtype, const SelScanArgs& a, cudaStream_t s);
 
+// rows of row_bytes (a multiple of 16), ld_bytes apart: zeros in those from *end on (end given) or with a negative slot
+cudaError_t launch_clear_rows(void* y, int64_t ld_bytes, int32_t row_bytes, int64_t rows, const int32_t* end,
+                              const int32_t* slots, cudaStream_t s);
+
 constexpr int32_t kMaxNormDim = 32768;
 struct NormArgs {
   const void* y;

@@ -218,7 +218,7 @@ class SsmMixer:
     ``weights``: W_in [2 Di, D], W_x [Di + 2 N, Di] (rows dt, B, C), W_O [D, Di] bf16 in [out, in] layout; conv_w
     [Di, K], A [Di, N] f32; conv_b, bias (of the step), skip [Di] f32 or absent.  D and Di are multiples of 64.
     ``max_tokens`` bounds a call's token rows; the buffers are made once.  Rows of no sequence (behind the last
-    prompt, or with slot -1 in a step) come back with nothing of use in them."""
+    prompt, or with slot -1 in a step) come back as zeros."""
 
     def __init__(self, D, Di, N, K, weights, max_tokens, device="cuda", alloc=None):
         bf, f32 = torch.bfloat16, torch.float32
@@ -268,6 +268,7 @@ class SsmMixer:
         steps()
         A.selective_scan(b["u"], b["dt"], w["bias"], w["A"], b["B"], b["C"], seqs, b["s"], skip=w["skip"], z=b["z"],
                          state=ssm, workspace=self.workspace, status=self.status, stream=stream)
+        A.clear_rows(b["s"], seqs=seqs, stream=stream)      # W_O makes zeros of zeros
         out()
         return b["y"]
 
@@ -280,6 +281,8 @@ class SsmMixer:
         steps()
         A.scan_step(b["u"], b["dt"], w["bias"], w["A"], b["B"], b["C"], ssm, b["s"], skip=w["skip"], z=b["z"], slots=slots,
                     status=self.status, stream=stream)
+        if slots is not None:
+            A.clear_rows(b["s"], slots=slots, stream=stream)
         out()
         return b["y"]
 
@@ -290,7 +293,8 @@ class Block:
     ``w_pre`` [D] f32 is the norm ahead of the mixer, ``w_post`` (or None) the norm behind it, ``scale`` (or None)
     a per-channel residual scale beside the number ``alpha``.  The residual stream r (bf16 or f32) is updated in
     place.  The pass that adds y to r also makes the next block's input: hand its ``w_pre`` over as ``next_norm``
-    and give the returned h to the next block, whose own first norm then falls away.
+    and give the returned h to the next block, whose own first norm then falls away.  Where the mixer gives zeros
+    (``SsmMixer``: rows of no sequence) r stays as it was (with eps > 0, whose norm of zeros is zero).
 
     ``h`` is what the mixer read in the block's last ``forward`` (handed in or made here): around a Layer it is the
     x of ``Layer.cache_from_prefill``.  A block that makes its input itself keeps the buffers of it, one for

@@ -119,3 +119,62 @@ def test_block_says_what_the_mixer_read(norms):
     given = torch.zeros(8, D, dtype=BF)
     blk.forward(r, h=given)
     assert blk.h is given
+
+
+# ---------------------------------------------------------------- rows of no sequence
+FAKE = 1 << 20
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=7), A.ERR_UNSUPPORTED), (dict(y=None), A.ERR_INVALID_ARG), (dict(y=FAKE + 8), A.ERR_INVALID_ARG),
+    (dict(D=60), A.ERR_INVALID_ARG), (dict(D=0), A.ERR_INVALID_ARG), (dict(ldy=56), A.ERR_INVALID_ARG),
+    (dict(ldy=68), A.ERR_INVALID_ARG), (dict(seqs=None), A.ERR_INVALID_ARG), (dict(slots=FAKE), A.ERR_INVALID_ARG),
+    (dict(seqs=None, slots=FAKE, B=0), A.ERR_INVALID_ARG), (dict(seqs=None, slots=FAKE, B=(1 << 20) + 1), A.ERR_UNSUPPORTED),
+    (dict(seqs=A.SeqsT(FAKE, None, None, 0, 2)), A.ERR_INVALID_ARG), (dict(seqs=A.SeqsT(None, None, None, 9, 2)), A.ERR_INVALID_ARG),
+    (dict(seqs=A.SeqsT(FAKE, None, None, 9, 1 << 21)), A.ERR_UNSUPPORTED)])
+def test_clear_rows_refuses(kw, code):
+    a = dict(dtype=A.BF16, y=FAKE, ldy=64, D=64, seqs=A.SeqsT(FAKE, None, None, 16, 2), B=0, slots=None)
+    a.update(kw)
+    L = A.load()
+    assert L.attamba_clear_rows(a["dtype"], a["y"], a["ldy"], a["D"], a["seqs"], a["B"], a["slots"], None) == code
+    assert L.attamba_last_error().startswith(b"attamba_clear_rows: ")
+
+
+def test_clear_rows_takes_no_cpu_tensor():
+    with pytest.raises(A.AttambaError, match="CUDA"):
+        A.clear_rows(torch.zeros(4, 64), slots=torch.zeros(4, dtype=torch.int32))
+
+
+class Recorder:
+    """attamba's calls as a list of their names, with the rows that clear_rows got."""
+
+    def __init__(self, monkeypatch):
+        self.calls = []
+        for name in ("proj_gemm", "causal_conv", "conv_step", "selective_scan", "scan_step", "clear_rows"):
+            monkeypatch.setattr(A, name, lambda *a, _n=name, **kw: self.calls.append((_n, a, kw)))
+
+
+def mixer_on_the_cpu(D=64, Di=128, N=16, K=4, rows=8):
+    z = lambda *s, dt=BF: torch.zeros(*s, dtype=dt)  # noqa: E731
+    w = dict(W_in=z(2 * Di, D), W_x=z(Di + 2 * N, Di), W_O=z(D, Di), conv_w=z(Di, K, dt=torch.float32),
+             A=z(Di, N, dt=torch.float32))
+    return layer.SsmMixer(D, Di, N, K, w, rows, device="cpu")
+
+
+def test_mixer_clears_rows_of_no_sequence_ahead_of_the_output_product(monkeypatch):
+    mix = mixer_on_the_cpu()
+    rec = Recorder(monkeypatch)
+    state, seqs, slots = mix.new_state(4), object(), torch.zeros(5, dtype=torch.int32)
+    names = lambda: [n for n, _, _ in rec.calls]  # noqa: E731
+    mix.forward(torch.zeros(7, 64, dtype=BF), seqs, state=state)
+    assert names() == ["proj_gemm", "causal_conv", "proj_gemm", "selective_scan", "clear_rows", "proj_gemm"]
+    _, a, kw = rec.calls[4]
+    assert a[0].data_ptr() == mix.buf["s"].data_ptr() and a[0].shape[0] == 7 and kw["seqs"] is seqs
+    assert rec.calls[5][1][0].data_ptr() == a[0].data_ptr()
+    rec.calls.clear()
+    mix.decode_step(state, torch.zeros(5, 64, dtype=BF), slots=slots)
+    assert names() == ["proj_gemm", "conv_step", "proj_gemm", "scan_step", "clear_rows", "proj_gemm"]
+    assert rec.calls[4][2]["slots"] is slots and rec.calls[4][1][0].shape[0] == 5
+    rec.calls.clear()
+    mix.decode_step(state, torch.zeros(4, 64, dtype=BF))          # every row has its state: nothing to clear
+    assert "clear_rows" not in names()
