@@ -129,6 +129,7 @@ class Layer:
         self.prefill = Prefill(B, n, D, H, dh, N, n_chunks, bf, device=device, alloc=alloc)
         self.y = alloc((T, D), bf)
         self.status = self.prefill.status
+        self.device = self.status.device
         self._step = None   # decode buffers, made by the first decode_step
 
     @property
@@ -205,6 +206,17 @@ class Layer:
         return self.y
 
 
+def _check_device(own, t, stream, what):
+    """The projections launch on the current device and the SSM block's operators on their tensors': tensors, stream and
+    current device must be where ``own`` is."""
+    if t.device != own:
+        raise A.AttambaError(f"{what} is on {own}, its input on {t.device}")
+    if own.type == "cuda":
+        if torch.cuda.current_device() != own.index:
+            raise A.AttambaError(f"{what}: {own} is not the current device")
+        if stream is not None and stream.device_index != own.index:
+            raise A.AttambaError(f"{what} is on {own}, the stream is on cuda:{stream.device_index}")
+
 
 class SsmMixer:
     """A Mamba block's mixer: the layer's selective SSM over whole sequences, with its short convolution, skip
@@ -218,7 +230,7 @@ class SsmMixer:
     ``weights``: W_in [2 Di, D], W_x [Di + 2 N, Di] (rows dt, B, C), W_O [D, Di] bf16 in [out, in] layout; conv_w
     [Di, K], A [Di, N] f32; conv_b, bias (of the step), skip [Di] f32 or absent.  D and Di are multiples of 64.
     ``max_tokens`` bounds a call's token rows; the buffers are made once.  Rows of no sequence (behind the last
-    prompt, or with slot -1 in a step) come back as zeros."""
+    prompt, or with slot -1 in a step) come back as zeros.  Calls are made with the mixer's device current."""
 
     def __init__(self, D, Di, N, K, weights, max_tokens, device="cuda", alloc=None):
         bf, f32 = torch.bfloat16, torch.float32
@@ -239,6 +251,12 @@ class SsmMixer:
         self.buf = {k: alloc((max_tokens, n), bf) for k, n in widths.items()}
         self.workspace = torch.empty(A.selective_scan_workspace_size(max_tokens, Di, N), dtype=torch.uint8, device=device)
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.device = self.status.device
+        for name, t in self.w.items():
+            if t is not None and t.device != self.device:
+                raise A.AttambaError(f"{name} must be on {self.device}, got {t.device}")
+        if any(b.device != self.device for b in self.buf.values()):
+            raise A.AttambaError(f"alloc must give buffers on {self.device}")
 
     def new_state(self, slots):
         """Carried states of ``slots`` sequences, all at zero: (convolution window, SSM state)."""
@@ -261,6 +279,7 @@ class SsmMixer:
     def forward(self, h, seqs, state=None, stream=None):
         """h [T, D] bf16 over the sequences of ``seqs`` (attamba.Seqs) -> y [T, D] (the mixer's own buffer); ``state``
         as from new_state, updated in place."""
+        _check_device(self.device, h, stream, "this mixer")
         b, w = self._rows(h.shape[0]), self.w
         win, ssm = (None, None) if state is None else state
         steps, out = self._ends(h, b, stream)
@@ -274,6 +293,7 @@ class SsmMixer:
 
     def decode_step(self, state, h_t, slots=None, stream=None):
         """One new token per sequence: h_t [B, D] bf16 -> y_t [B, D]; ``slots`` [B] int32 names the state rows."""
+        _check_device(self.device, h_t, stream, "this mixer")
         b, w = self._rows(h_t.shape[0]), self.w
         win, ssm = state
         steps, out = self._ends(h_t, b, stream)
@@ -317,6 +337,7 @@ class Block:
         return kept[-1][:r.shape[0]]
 
     def _input(self, r, h, kept, first, stream):
+        _check_device(getattr(self.mixer, "device", r.device), r, stream, "this block")
         if h is None:
             h = self._buffer(kept, r, first, stream)
             A.block_norm(None, r, h=h, w_pre=self.w_pre, eps=self.eps, stream=stream)

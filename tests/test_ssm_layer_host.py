@@ -178,3 +178,76 @@ def test_mixer_clears_rows_of_no_sequence_ahead_of_the_output_product(monkeypatc
     rec.calls.clear()
     mix.decode_step(state, torch.zeros(4, 64, dtype=BF))          # every row has its state: nothing to clear
     assert "clear_rows" not in names()
+
+
+# ---------------------------------------------------------------- devices
+class Rows:
+    """What a device check reads of a tensor."""
+
+    def __init__(self, device, shape=(4, 64)):
+        self.device, self.shape, self.dtype = torch.device(device), torch.Size(shape), BF
+
+
+class Stream:
+    def __init__(self, index):
+        self.device_index = index
+
+
+@pytest.mark.parametrize("where,current,stream,match", [
+    ("cuda:1", 0, None, "cuda:1 is not the current device"), ("cuda:0", 0, None, "on cuda:0"),
+    ("cuda:1", 1, Stream(0), "stream is on cuda:0"), ("cpu", 1, None, "on cpu")])
+def test_mixer_and_block_refuse_another_device(monkeypatch, norms, where, current, stream, match):
+    """The projections launch on the current device, the other operators on their tensors': a mixer whose buffers are on
+    cuda:1 takes tensors and streams of cuda:1 with cuda:1 current, and says so before any call."""
+    mix = mixer_on_the_cpu()
+    mix.device = torch.device("cuda", 1)
+    blk = layer.Block(mix, torch.ones(64))
+    rec = Recorder(monkeypatch)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    for call in (lambda: mix.forward(Rows(where), None, stream=stream), lambda: mix.decode_step((None, None), Rows(where), stream=stream),
+                 lambda: blk.forward(Rows(where), None, stream=stream), lambda: blk.decode_step((None, None), Rows(where), stream=stream)):
+        with pytest.raises(A.AttambaError, match=match):
+            call()
+    assert not rec.calls and not norms
+
+
+def test_mixer_runs_where_its_buffers_are(monkeypatch):
+    mix = mixer_on_the_cpu()
+    mix.device = torch.device("cuda", 1)
+    rec = Recorder(monkeypatch)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    mix.decode_step((None, None), Rows("cuda:1"), stream=Stream(1))
+    assert rec.calls
+
+
+def test_block_around_a_layer_refuses_another_device(monkeypatch, norms):
+    class Lay(Mixer):
+        device = torch.device("cuda", 0)
+
+    blk = layer.Block(Lay(4, 64), torch.ones(64))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(A.AttambaError, match="on cuda:1"):
+        blk.forward(Rows("cuda:1"))
+    with pytest.raises(A.AttambaError, match="cuda:0 is not the current device"):
+        blk.forward(Rows("cuda:0"), h=Rows("cuda:0"))
+    assert not norms
+
+
+@pytest.mark.parametrize("name", ["W_in", "W_x", "W_O", "conv_w", "A", "bias"])
+def test_mixer_refuses_weights_on_another_device(name):
+    D, Di, N, K = 64, 128, 16, 4
+    z = lambda *s, dt=BF: torch.zeros(*s, dtype=dt)  # noqa: E731
+    f32 = torch.float32
+    w = dict(W_in=z(2 * Di, D), W_x=z(Di + 2 * N, Di), W_O=z(D, Di), conv_w=z(Di, K, dt=f32), A=z(Di, N, dt=f32), bias=z(Di, dt=f32))
+    w[name] = w[name].to("meta")
+    with pytest.raises(A.AttambaError, match=f"{name} must be on cpu, got meta"):
+        layer.SsmMixer(D, Di, N, K, w, 8, device="cpu")
+
+
+def test_mixer_refuses_buffers_on_another_device():
+    with pytest.raises(A.AttambaError, match="buffers"):
+        D, Di, N, K = 64, 128, 16, 4
+        z = lambda *s, dt=BF: torch.zeros(*s, dtype=dt)  # noqa: E731
+        f32 = torch.float32
+        w = dict(W_in=z(2 * Di, D), W_x=z(Di + 2 * N, Di), W_O=z(D, Di), conv_w=z(Di, K, dt=f32), A=z(Di, N, dt=f32))
+        layer.SsmMixer(D, Di, N, K, w, 8, device="cpu", alloc=lambda shape, dt: torch.empty(shape, dtype=dt, device="meta"))
