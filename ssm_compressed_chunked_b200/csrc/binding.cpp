@@ -136,6 +136,7 @@ bool state(PyObject* o, c10::ScalarType dt, int64_t r, int64_t c, int dev, State
   const at::Tensor* t = tensor(o, "state");
   if (!t) return false;
   const int64_t shape[3] = {t->dim() == 3 ? t->size(0) : -1, r, c};
+  if (shape[0] == 0) return refuse("state has no slots");   // its address is null, which would mean no state
   if (shape[0] > INT32_MAX) return refuse("state has too many slots");
   out.n = (int32_t)shape[0];
   return dense(o, "state", dt, shape, dev, out.p);
