@@ -130,8 +130,10 @@ def load():
 def _check(st, what):
     if st != OK:
         L = load()
-        raise AttambaError(f"{what}: {L.attamba_status_string(st).decode()} "
-                           f"{L.attamba_last_error().decode()}".strip())
+        why = L.attamba_last_error().decode()
+        if st != ERR_CUDA and not why.startswith(what + ":"):
+            why = ""     # this refusal gives no reason; the text is an earlier one's
+        raise AttambaError(f"{what}: {L.attamba_status_string(st).decode()} {why}".strip())
 
 
 def _stream(stream):
