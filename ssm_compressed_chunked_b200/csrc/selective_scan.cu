@@ -262,6 +262,14 @@ __global__ void __launch_bounds__(kThreads, MINB) scan_tile_kernel(SelScanArgs p
   // tokens [a, b), all of one sequence, next to those walked before; by the whole block
   auto walk = [&](int a, int b) {
     if (!in_bounds(a >= w0 && b <= t1 && t1 <= p.T, p.status)) return;   // the same for every thread
+    // decay_fma2 makes a number of a NaN; one in A reaches the state here (one in delta through delta x B)
+#pragma unroll
+    for (int c = 0; c < CPT; ++c)
+#pragma unroll
+      for (int q = 0; q < POLY; ++q) {
+        if (isnan(a2[c][q].x)) h[c][q].x = a2[c][q].x;
+        if (isnan(a2[c][q].y)) h[c][q].y = a2[c][q].y;
+      }
     for (int t = a; t < b;) {
       const int k = (t - w0) / W;
       if (k != window) {
