@@ -1,17 +1,19 @@
-"""layer.Block on the GPU beyond the plain call: a caller's stream, handing a prefill through a block to decoding."""
+"""layer.Block on the GPU: a caller's stream, handing a prefill through a block to decoding, the values of its decode steps."""
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
-from block_cases import offsets
+from block_cases import HALF, TINY, U, assert_within, offsets, scan_bound
 from helpers import f64
+from oracle import block as OB
 from ssm_compressed_chunked_b200 import attamba as A
 from ssm_compressed_chunked_b200 import layer
 from ssm_compressed_chunked_b200 import workloads as W
-from test_gpu_ssm_block import i32
-from test_gpu_ssm_layer import BF, cuda, mixer_weights
+from test_gpu_ssm_block import conv_bound, i32
+from test_gpu_ssm_layer import BF, cuda, gemm_check, mixer_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +87,93 @@ def test_prefill_through_a_block_hands_over_to_decoding():
     a, _ = blk.decode_step(got, t0.clone())
     b, _ = blk.decode_step(want, t0.clone())
     assert torch.equal(a, b) and lay.status.item() == 0 and bool(f64(a).any())
+
+
+def norm_of(r, w):
+    """The bf16 norm ahead of a mixer, from the operator itself."""
+    h = torch.empty(r.shape, dtype=BF, device="cuda")
+    A.block_norm(None, r, h=h, w_pre=w)
+    return h
+
+
+def check_join(r, h, y, r0, post, scale, alpha, pre, res):
+    """A block's residual sum and next input against the oracle on the mixer's own output."""
+    ref, ref_h = OB.block_norm(f64(y), f64(r0), w_post=f64(post), w_pre=f64(pre), scale=f64(scale),
+                               alpha=float(np.float32(alpha)))
+    v = np.abs(ref - f64(r0))
+    # fp32 steps: the norm's sum and root and three products of the block's share, one sum; then the stored rounding
+    dr = 60 * U * v + 2 * U * (np.abs(ref) + np.abs(f64(r0)))
+    assert_within(f64(r), ref, dr + HALF[res] * (np.abs(ref) + dr) + TINY, "r")
+    rms = np.sqrt((ref * ref).mean(axis=1, keepdims=True) + 1e-5)
+    rel = np.sqrt((dr * dr).sum(axis=1, keepdims=True) / (ref * ref).sum(axis=1, keepdims=True))
+    dh = np.abs(f64(pre)) / rms * dr + np.abs(ref_h) * (60 * U + rel)
+    assert_within(f64(h), ref_h, dh + HALF[BF] * (np.abs(ref_h) + dh) + TINY, "h")
+
+
+@pytest.mark.parametrize("res", [torch.float32, BF])
+@pytest.mark.parametrize("N,K,slots", [(16, 4, None), (32, 3, [4, -1, 0, 2, 5])])
+def test_block_decode_step_around_the_mixer_has_the_oracles_values(res, N, K, slots):
+    """Every stage of a decode step through a block against the oracle, each fed the GPU's own input to it: the norm ahead,
+    the mixer's six stages with both states, the join with post-norm, scale and the next block's norm."""
+    D, Di, B = 128, 256, 5
+    g = torch.Generator().manual_seed(N)
+    w = mixer_weights(D, Di, N, K, N)
+    mix = layer.SsmMixer(D, Di, N, K, cuda(w), B)
+    pre, post, scale, nn = (torch.rand(D, generator=g).cuda() + 0.5 for _ in range(4))
+    blk = layer.Block(mix, pre, w_post=post, scale=scale, alpha=0.6)
+    win, ssm = mix.new_state(6)
+    win.copy_(torch.randn(win.shape, generator=g))
+    ssm.copy_(torch.randn(ssm.shape, generator=g))
+    r = torch.randn(B, D, generator=g).to(res).cuda()
+    live = np.array([s >= 0 for s in (slots or range(B))])
+    for _ in range(3):
+        r0, win0, ssm0 = r.clone(), win.cpu().clone(), ssm.cpu().clone()
+        h0 = norm_of(r0, pre)
+        ref = OB.norm(f64(r0), f64(pre), 1e-5)
+        assert_within(f64(h0), ref, (HALF[BF] + 60 * U) * np.abs(ref) + TINY, "norm ahead")
+        # the mixer called alone on copies of the states gives the y that the block's join read
+        y = mix.decode_step((win.clone(), ssm.clone()), h0, slots=i32(slots)).clone()
+        r, h = blk.decode_step((win, ssm), r, slots=i32(slots), next_norm=nn)
+        assert mix.status.item() == 0
+        b = {k: v[:B].cpu()[live] for k, v in mix.buf.items()}
+        gemm_check(b["x"], h0.cpu()[live], w["W_in"][:Di], "x")
+        gemm_check(b["z"], h0.cpu()[live], w["W_in"][Di:], "z")
+        sl = np.asarray(slots if slots else range(B))[live]
+        m = int(live.sum())
+        args = (f64(b["x"]), f64(w["conv_w"]), f64(w["conv_b"]), offsets([1] * m), f64(win0), sl, np.ones(m, dtype=int))
+        lin, _ = OB.causal_conv(*args, act="linear")
+        ref, ref_win = OB.causal_conv(*args)
+        assert_within(f64(b["u"]), ref, conv_bound(b["x"], w["conv_w"], w["conv_b"], lin, ref, offsets([1] * m), BF, "silu", win0,
+                                                   sl, np.ones(m, dtype=int)), "u")
+        assert np.array_equal(f64(win), ref_win)
+        for name, rows in (("dt", slice(0, Di)), ("B", slice(Di, Di + N)), ("C", slice(Di + N, Di + 2 * N))):
+            gemm_check(b[name], b["u"], w["W_x"][rows], name)
+        d = dict(x=b["u"], dt=b["dt"], B=b["B"], C=b["C"], z=b["z"], A=w["A"], bias=w["bias"], skip=w["skip"])
+        ref, ref_ssm = OB.selective_scan(f64(b["u"]), f64(b["dt"]), f64(w["bias"]), f64(w["A"]), f64(b["B"]), f64(b["C"]),
+                                         offsets([1] * m), f64(w["skip"]), f64(b["z"]), f64(ssm0), sl, np.ones(m, dtype=int))
+        by, bst = scan_bound(d, offsets([1] * m), BF, ssm0, sl, np.ones(m, dtype=int))
+        assert_within(f64(b["s"]), ref, by, "s")
+        assert_within(f64(ssm)[sl], ref_ssm[sl], bst[sl], "ssm state")
+        gemm_check(y.cpu()[live], b["s"], w["W_O"], "y")
+        check_join(r, h, y, r0, post, scale, 0.6, nn, res)
+
+
+@pytest.mark.parametrize("res", [torch.float32, BF])
+def test_block_decode_step_around_the_layer_has_the_oracles_values(res):
+    """The layer's own decode step is compared with the oracle elsewhere; here the block's norm ahead of it and the join behind
+    it, with the layer called alone on an equal cache."""
+    B, H, D = 3, 2, 128
+    g = torch.Generator().manual_seed(12)
+    lay = attamba_layer(B, 64, H, g)
+    pre, post, scale, nn = (torch.rand(D, generator=g).cuda() + 0.5 for _ in range(4))
+    blk = layer.Block(lay, pre, w_post=post, scale=scale, alpha=0.6)
+    one, two = lay.new_cache(16), lay.new_cache(16)
+    r = torch.randn(B, D, generator=g).to(res).cuda()
+    for _ in range(10):          # past the first chunk's end
+        r0 = r.clone()
+        y = lay.decode_step(one, norm_of(r0, pre)).clone()
+        r, h = blk.decode_step(two, r, next_norm=nn)
+        check_join(r, h, y, r0, post, scale, 0.6, nn, res)
+    for k in ("state", "Kb", "Vb", "bpos", "Kr", "Vr", "nb", "pos"):
+        assert torch.equal(getattr(one, k), getattr(two, k)), k
+    assert lay.status.item() == 0 and int(one.nb.min()) >= 1
