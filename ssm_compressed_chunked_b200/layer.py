@@ -337,6 +337,8 @@ class Block:
         return kept[-1][:r.shape[0]]
 
     def _input(self, r, h, kept, first, stream):
+        if len(r.shape) != 2:
+            raise A.AttambaError(f"r must be [rows, D], got {list(r.shape)}")
         _check_device(getattr(self.mixer, "device", r.device), r, stream, "this block")
         if h is None:
             h = self._buffer(kept, r, first, stream)

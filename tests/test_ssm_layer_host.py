@@ -251,3 +251,12 @@ def test_mixer_refuses_buffers_on_another_device():
         f32 = torch.float32
         w = dict(W_in=z(2 * Di, D), W_x=z(Di + 2 * N, Di), W_O=z(D, Di), conv_w=z(Di, K, dt=f32), A=z(Di, N, dt=f32))
         layer.SsmMixer(D, Di, N, K, w, 8, device="cpu", alloc=lambda shape, dt: torch.empty(shape, dtype=dt, device="meta"))
+
+
+@pytest.mark.parametrize("shape", [(64,), (2, 3, 64)])
+def test_block_refuses_a_stream_that_is_not_rows(norms, shape):
+    blk = layer.Block(Mixer(8, 64), torch.ones(64))
+    for call in (lambda: blk.forward(torch.zeros(shape)), lambda: blk.decode_step(None, torch.zeros(shape))):
+        with pytest.raises(A.AttambaError, match=r"r must be \[rows, D\]"):
+            call()
+    assert not norms
