@@ -165,3 +165,103 @@ def test_scan_across_more_tiles_than_a_join_walks_at_once(N, lens):
                                     n["skip"], n["z"][last:])
         off = np.abs(lost - ref[last:]) / by[last:]
         assert np.median(off[-500:]) > 2
+
+
+# ---------------------------------------------------------------- the documented limits
+def gpu_inputs(T, D, N, seed):
+    """scan_inputs' distributions in bf16, made on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    u = lambda *s: torch.rand(*s, generator=g, device="cuda")  # noqa: E731
+    return dict(x=n(T, D), dt=n(T, D), B=n(T, N), C=n(T, N), z=n(T, D), A=-torch.exp(u(D, N) * np.log(16.0)), skip=u(D) - 0.5,
+                bias=torch.log(torch.expm1(torch.exp(u(D) * np.log(100.0) + np.log(1e-3)))))
+
+
+@pytest.mark.parametrize("T,lens", [(3, [2, 1]), (130, [100, 0, 29])])
+def test_the_widest_rows(T, lens):
+    """2^20 channels, the most that a call takes: prompts in a single tile of one or many windows, and steps."""
+    D, N, K, S = 1 << 20, 16, 4, len(lens)
+    bf = torch.bfloat16
+    d = gpu_inputs(T, D, N, T)
+    cu, cont = offsets(lens), [1] * S
+    g = torch.Generator(device="cuda").manual_seed(1)
+    state = torch.randn(S, N, D, generator=g, device="cuda")
+    win = torch.randn(S, K - 1, D, generator=g, device="cuda").to(bf)
+    w = torch.randn(D, K, generator=g, device="cuda")
+    seqs, status = A.Seqs(i32(cu), T, cont=i32(cont)), new_status()
+    ws = A.selective_scan_workspace_size(T, D, N)
+    y, cy = torch.full((T, D), float("nan"), dtype=bf, device="cuda"), torch.full((T, D), float("nan"), dtype=bf, device="cuda")
+    st, wn = state.clone(), win.clone()
+    A.selective_scan(d["x"], d["dt"], d["bias"], d["A"], d["B"], d["C"], seqs, y, skip=d["skip"], z=d["z"], state=st,
+                     workspace=torch.empty(ws, dtype=torch.uint8, device="cuda") if ws else None, status=status)
+    A.causal_conv(d["x"], w, None, seqs, cy, state=wn, status=status)
+    ys, cs = torch.full((S, D), float("nan"), dtype=bf, device="cuda"), torch.full((S, D), float("nan"), dtype=bf, device="cuda")
+    st1, wn1 = state.clone(), win.clone()
+    A.scan_step(d["x"][:S], d["dt"][:S], d["bias"], d["A"], d["B"][:S], d["C"][:S], st1, ys, skip=d["skip"], z=d["z"][:S],
+                status=status)
+    A.conv_step(d["x"][:S], w, None, wn1, cs, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    pick = [0, 1, 255, 256, 4095, 4096, D // 2 - 1, D // 2, D - 129, D - 128, D - 2, D - 1]
+    part = {k: v.cpu() for k, v in channels_of(d, pick).items()}
+    init, iw, pw = state[:, :, pick].cpu(), win[:, :, pick].cpu(), w[pick].cpu()
+    m = sum(lens)
+    for rows, tab, got_y, got_st, got_c, got_w in ((T, cu, y, st, cy, wn), (S, offsets([1] * S), ys, st1, cs, wn1)):
+        p = {k: (v[:rows] if k in ("x", "dt", "B", "C", "z") else v) for k, v in part.items()}
+        n = {k: f64(v) for k, v in p.items()}
+        live = min(m, rows)
+        ref, ref_st = OB.selective_scan(n["x"], n["dt"], n["bias"], n["A"], n["B"], n["C"], tab, n["skip"], n["z"], f64(init),
+                                        None, cont)
+        by, bst = scan_bound(p, tab, bf, init, None, cont)
+        assert_within(f64(got_y[:live, pick]), ref[:live], by[:live], "scan y")
+        assert_within(f64(got_st[:, :, pick]), ref_st, bst, "scan state")
+        pre, _ = OB.causal_conv(n["x"], f64(pw), None, tab, f64(iw), None, cont, act="linear")
+        ref, ref_w = OB.causal_conv(n["x"], f64(pw), None, tab, f64(iw), None, cont)
+        b = conv_bound(p["x"], pw, None, pre, ref, tab, bf, "silu", iw, None, cont)
+        assert_within(f64(got_c[:live, pick]), ref[:live], b[:live], "conv y")
+        assert np.array_equal(f64(got_w[:, :, pick]), ref_w)
+    assert bool(torch.isnan(y[m:]).all()) and bool(torch.isnan(cy[m:]).all())
+    assert not bool(torch.isnan(y[:m]).any()) and not bool(torch.isnan(cy[:m]).any())
+
+
+def test_the_most_sequences():
+    """2^20 sequences of no, one and two tokens without a slot map, half of them continuing; compared on samples from both
+    ends and between."""
+    S, D, N, K = 1 << 20, 8, 16, 4
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 3, S)
+    lens[-40:] = 0
+    cu = offsets(lens)
+    T = int(cu[-1]) + 5
+    cont = rng.integers(0, 2, S)
+    d = gpu_inputs(T, D, N, 9)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    state = torch.randn(S, N, D, generator=g, device="cuda")
+    win = torch.randn(S, K - 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(D, K, generator=g, device="cuda")
+    seqs, status = A.Seqs(i32(cu), T, cont=i32(cont)), new_status()
+    y, cy = (torch.full((T, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    st, wn = state.clone(), win.clone()
+    ws = torch.empty(A.selective_scan_workspace_size(T, D, N), dtype=torch.uint8, device="cuda")
+    A.selective_scan(d["x"], d["dt"], d["bias"], d["A"], d["B"], d["C"], seqs, y, skip=d["skip"], z=d["z"], state=st,
+                     workspace=ws, status=status)
+    A.causal_conv(d["x"], w, None, seqs, cy, state=wn, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0 and bool(torch.isnan(y[T - 5:]).all()) and not bool(torch.isnan(y[:T - 5]).any())
+    for a in (0, S // 3, S // 2 + 17, S - 300):
+        b = a + 300
+        t0, t1 = int(cu[a]), int(cu[b])
+        sub, c = (cu[a:b + 1] - t0).astype(np.int32), cont[a:b]
+        p = {k: (v[t0:t1] if k in ("x", "dt", "B", "C", "z") else v).cpu() for k, v in d.items()}
+        n = {k: f64(v) for k, v in p.items()}
+        init, iw = state[a:b].cpu(), win[a:b].cpu()
+        ref, ref_st = OB.selective_scan(n["x"], n["dt"], n["bias"], n["A"], n["B"], n["C"], sub, n["skip"], n["z"], f64(init),
+                                        None, c)
+        by, bst = scan_bound(p, sub, torch.bfloat16, init, None, c)
+        assert_within(f64(y[t0:t1]), ref, by, "scan y")
+        assert_within(f64(st[a:b]), ref_st, bst, "scan state")
+        pre, _ = OB.causal_conv(n["x"], f64(w), None, sub, f64(iw), None, c, act="linear")
+        ref, ref_w = OB.causal_conv(n["x"], f64(w), None, sub, f64(iw), None, c)
+        assert_within(f64(cy[t0:t1]), ref, conv_bound(p["x"], w.cpu(), None, pre, ref, sub, torch.bfloat16, "silu", iw, None, c),
+                      "conv y")
+        assert np.array_equal(f64(wn[a:b]), ref_w)
