@@ -11,7 +11,8 @@
 // from the first load to the last store, so the two means cost two reductions and
 // no second read.  Sums of squares are fp32: a thread's share first, then the warp's
 // tree, then the warps' partial sums.  16384 x 2048 bf16 with gate and fp32 residual:
-// 70-77 us by box, 6.1-6.6 TB/s, the copy rate.
+// 71 us in a graph of such calls, 78 with other work between them, 6.0-6.6 TB/s (93-103%
+// of the copy rate); f32 throughout, no gate: 82 us, 6.5 TB/s.
 #include "common.cuh"
 #include "launch.h"
 
@@ -187,9 +188,10 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
 
 template <typename T, typename R>
 cudaError_t launch_for(const NormArgs& a, cudaStream_t s) {
-  // threads a row and vectors a thread, measured (B200, GB/s of the copy's 6470): rows of 256 6050, 512 5510, 1024 6180,
-  // 2048 5660 (6640 with an fp32 residual), 4096 5680, 8192 5080, 16384 4330, 32768 3650; from 16384 on an SM holds too
-  // few rows to overlap one's sums with another's loads
+  // threads a row and vectors a thread, measured (B200, bf16 with a SiLU gate and both norms, 33.5M elements, GB/s of the
+  // copy's 6470 with a bf16 / an fp32 residual): rows of 256 6500 / 6620, 512 6470 / 6640, 1024 6390 / 6640, 2048 6180 / 6600,
+  // 4096 5230 / 5860, 8192 4860 / 5460, 16384 4140 / 4680, 32768 3550 / 4330; from 4096 on an SM holds too few rows to
+  // overlap one's sums with another's loads
   const int vecs = a.D / 8;
   if (vecs <= 32) return launch<T, R, 32, 1>(a, s);
   if (vecs <= 64) return launch<T, R, 64, 1>(a, s);

@@ -13,9 +13,12 @@
 // neighbouring channels, a block four warps of one run.  Rows come through a ring of
 // the thread's own in shared memory, 16 rows deep (cp.async, no barrier): held in
 // registers, the same rows in flight cost the blocks that hide the latency.
-// 32768 x 2048 bf16, K 4: 49 us, 5.4 TB/s (84% of the copy rate); rows loaded
-// into registers four or eight at a time 62, sixteen 74, one batch ahead 60-70.
-// SiLU takes two operations an element on the multi-function unit (65% busy).
+// 32768 x 2048, K 4, bf16: 50 us in a graph of such calls, 52 with other work between
+// them, 5.1-5.4 TB/s (80-83% of the copy rate); f32 88 us, 6.1 TB/s (94%).  bf16 rows
+// loaded into registers four or eight at a time 62, sixteen 74, one batch ahead 60-70.
+// SiLU takes two operations an element on the multi-function unit (65% busy in bf16).
+// A width that leaves most of the last block's warps without channels pays for them:
+// 32768 x 640 bf16 25 us, x 512 18.
 //
 // Ownership.  The run that holds a sequence's first token (or an empty sequence's
 // place) also computes that sequence's first K-1 tokens when they pass the run's

@@ -29,8 +29,9 @@
 // What bounds it: the exponentials.  Both passes take T D N of them, on a unit that does
 // 16 a clock and SM, beside 4 (output) or 3 (state) half-rate f32x2 operations a pair: at
 // 16384 x 1024 x 16 (bf16, gated) that is 60 + 67 us at 1.9 GHz, and the call takes 176
-// (0.77 TB/s of 6.47).  The unit is 82% busy in the state pass, 69% in the output pass,
-// the issue slots 43 and 46%; three warps a scheduler is what the registers hold.  Measured and not kept: one channel a thread and five to seven blocks on an SM
+// (0.77 TB/s of 6.47): K tiles take the exponentials 2 - 1/K times, and K is 110 here.  The unit is
+// 82% busy in the state pass, 69% in the output pass, the issue slots 43 and 46%; three warps a scheduler
+// is what the registers hold.  Measured and not kept: one channel a thread and five to seven blocks on an SM
 // (196-221 us), two channels at four blocks (194), three quarters of the window (186),
 // all groups of a window unrolled (185), the short batches' tiles as a cluster that exchanges
 // states through distributed shared memory (61 tokens 9.9 us against 6.9 in a single tile).
@@ -524,8 +525,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) scan_join_kernel(SelScanArgs 
 // state accesses are 16 bytes a lane, 128 bytes of a state row a quarter.  A block walks several batch rows of its
 // 128 channels: A stays in registers, each thread copies its part of the next row's state into a ring of its own
 // (cp.async, no barrier) and loads the next row's inputs while it computes this one's.  Bound by reading and writing
-// the state: 251 rows x 2048 channels x 16 in 16.2 us (4.3 TB/s; a copy of these rows in the same pattern takes 14.9),
-// 256 x 4096 x 32 in 51 us (5.4 TB/s).  One row a block with everything in registers: 18.1 and 60.  The search for
+// the state: 251 rows x 2048 channels x 16 in 16.2-16.6 us (4.2 TB/s), 1024 rows in 53 (5.4), 256 x 4096 x 16 in 28 (5.2),
+// x 32 in 52 (5.3): with five rows a block the ring's fill and drain are a third of the call (a copy of these rows in the same
+// pattern takes 14.9); states that stay in the L2 take 11.8.  One row a block with everything in registers: 18.1 and 60.  The search for
 // repeated slots (a hash table of the block's rows): 4096 x 1024 x 16 in 113 us, 91 without a slot map, 188 with
 // every row compared with every slot ahead of it.
 template <typename T> struct Four;
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, step_blocks(NS)) scan_step_kernel(Se
 struct ScanPlan {
   int lpc, tile_len, tiles, groups;
 };
-constexpr int kSMs = 148;
+constexpr int kSMs = 148;   // a B200's: the workspace's size follows from it, and is asked for without a device
 constexpr int scan_cpt(int lpc, int NS) { return lpc <= 2 && NS == 16 ? 2 : 1; }
 constexpr int scan_blocks(int lpc) { return lpc == 1 ? 3 : lpc == 2 ? 4 : 5; }
 

@@ -225,7 +225,9 @@ class SsmMixer:
     pith.science review of Attamba, "Assumptions & free parameters": the SSM is Mamba's selective SSM (Section
     3.2, Eq. 3).  Here it is not chunked: its state runs through each sequence and is carried from call to call.
     One GEMM gives the SSM input and its gate, the convolution (with SiLU) the scan's input u, a second GEMM the
-    step and B, C from u, the scan its gated output, a third GEMM y.
+    step and B, C from u, the scan its gated output, a third GEMM y.  The step's projection is full-rank, as the
+    layer's are: a checkpoint whose step goes through a low rank r (dt = W_dt W_r u) has the two multiplied out into
+    the first Di rows of W_x, and pays Di x Di a token for them instead of 2 r Di.
 
     ``weights``: W_in [2 Di, D], W_x [Di + 2 N, Di] (rows dt, B, C), W_O [D, Di] bf16 in [out, in] layout; conv_w
     [Di, K], A [Di, N] f32; conv_b, bias (of the step), skip [Di] f32 or absent.  D and Di are multiples of 64.
