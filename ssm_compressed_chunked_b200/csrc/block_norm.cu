@@ -13,8 +13,8 @@
 // tree, then the warps' partial sums.  16384 x 2048 bf16 with gate and fp32 residual:
 // 71 us in a graph of such calls, 78 with other work between them, 6.0-6.6 TB/s (93-103%
 // of the copy rate); f32 throughout, no gate: 82 us, 6.5 TB/s.
-#include "common.cuh"
 #include "launch.h"
+#include "ssm_block.cuh"
 
 namespace attamba {
 

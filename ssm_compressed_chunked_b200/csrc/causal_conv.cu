@@ -24,8 +24,8 @@
 // place) also computes that sequence's first K-1 tokens when they pass the run's
 // end, and writes its window: the only thread that reads a carried window is then
 // the thread that replaces it, so no order between blocks is needed.
-#include "common.cuh"
 #include "launch.h"
+#include "ssm_block.cuh"
 
 namespace attamba {
 

@@ -37,8 +37,8 @@
 // states through distributed shared memory (61 tokens 9.9 us against 6.9 in a single tile).
 #include <type_traits>
 
-#include "common.cuh"
 #include "launch.h"
+#include "ssm_block.cuh"
 
 namespace attamba {
 
