@@ -326,17 +326,19 @@ class Block:
     def __init__(self, mixer, w_pre, w_post=None, scale=None, alpha=1.0, eps=1e-5):
         self.mixer, self.w_pre, self.w_post, self.scale, self.alpha, self.eps = mixer, w_pre, w_post, scale, alpha, eps
         self.h = None
-        self._prompt, self._step = [], []   # input buffers, the last one the largest
+        self._prompt, self._step = [], []   # input buffers, the last one of a width the largest
 
     def _buffer(self, kept, r, first, stream):
         """r.shape rows of bf16 that stay the block's.  Made on the stream that uses them, so that no other stream's
         pending work holds the memory; freed with the block alone, as a captured graph may hold an address."""
-        n = r.shape[0]
-        if not kept or kept[-1].shape[0] < n:
-            n = max(n, first if not kept else min(2 * kept[-1].shape[0], getattr(self.mixer, "max_tokens", n)))
+        n, D = r.shape
+        fit = [b for b in kept if b.shape[1] == D and b.device == r.device]   # others are left from refused calls
+        if not fit or fit[-1].shape[0] < n:
+            n = max(n, first if not fit else min(2 * fit[-1].shape[0], getattr(self.mixer, "max_tokens", n)))
             with torch.cuda.stream(stream):
-                kept.append(torch.empty(n, r.shape[1], dtype=torch.bfloat16, device=r.device))
-        return kept[-1][:r.shape[0]]
+                kept.append(torch.empty(n, D, dtype=torch.bfloat16, device=r.device))
+            fit = kept
+        return fit[-1][:r.shape[0]]
 
     def _input(self, r, h, kept, first, stream):
         if len(r.shape) != 2:

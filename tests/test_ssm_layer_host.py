@@ -260,3 +260,15 @@ def test_block_refuses_a_stream_that_is_not_rows(norms, shape):
         with pytest.raises(A.AttambaError, match=r"r must be \[rows, D\]"):
             call()
     assert not norms
+
+
+def test_a_refused_call_does_not_spoil_the_block(monkeypatch):
+    """A stream of a wrong width or device makes no buffer that later calls would be handed."""
+    D = 64
+    monkeypatch.setattr(A, "block_norm", lambda y, res, res_out=None, h=None, **kw: None)
+    mix = Mixer(16, D)
+    blk = layer.Block(mix, torch.ones(D))
+    for bad in (torch.zeros(16, 2 * D), torch.zeros(16, D, device="meta")):
+        blk.decode_step(None, bad)               # the library refuses these; here the recorders take them
+        blk.decode_step(None, torch.zeros(5, D))
+        assert mix.seen[-1].shape == (5, D) and mix.seen[-1].device.type == "cpu"
